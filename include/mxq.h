@@ -66,7 +66,8 @@ typedef int32_t mxq_status;
 /* Text for a status code (static storage, never NULL). */
 const char* mxq_status_string(mxq_status status);
 
-/* ABI version of this header (bumped on any signature change or added entry point). */
+/* ABI version of this header (bumped whenever an existing signature or meaning changes; an entry
+ * point that only joins the others leaves it). */
 int32_t mxq_abi_version(void);
 
 /* Checks that `device` is a gfx950 GPU and makes it current.  Every other
@@ -507,6 +508,98 @@ size_t mxq_moe_prepack_size(int64_t E, int64_t N, int64_t row_bytes);
 size_t mxq_moe_prepack_scales_size(int64_t E, int64_t N, int64_t groups);
 mxq_status mxq_moe_prepack(const void* w, int64_t E, int64_t N, int64_t row_bytes, void* out, void* stream);
 mxq_status mxq_moe_prepack_scales(const void* s, int64_t E, int64_t N, int64_t groups, void* out, void* stream);
+
+/* ------------------------------------------------------------------ expert routing
+ * Router logits -> the experts of each token and their weights, in the form the fused MoE takes
+ * (mxq_fused_moe_*: ids outside [0, E) drop their row).  Per token, with l its E logits:
+ *   live(e)  l[e] > -inf: a NaN or -inf logit (a masked expert, a padded row) takes its expert out
+ *   p[e]     MXQ_SCORE_SOFTMAX: exp(l[e] - max l) / sum over the live experts;
+ *            MXQ_SCORE_SIGMOID: 1 / (1 + exp(-l[e]))
+ *   pick[e]  p[e] + correction_bias[e] when a correction bias is given, else l[e]
+ *   groups   n_group > 1: E / n_group consecutive experts form a group, whose score is its largest
+ *            pick (MXQ_GROUP_MAX) or the sum of its two largest p + bias (MXQ_GROUP_TOP2); only the
+ *            topk_group best groups keep their experts (equal scores: the lower group)
+ *   chosen   the topk largest picks, largest first, equal picks by the lower expert; a slot that
+ *            finds no live expert gets id -1 and weight 0
+ *   weight   p of the chosen expert (without the bias); renormalize: divided by the sum over the
+ *            token's chosen experts; times scale
+ * Scores are fp32; picks closer than fp32 scores can tell apart are decided in 64 bits, so the
+ * chosen experts and their order are those of the exact scores.
+ *   logits           fp32 or bf16 (logits_dtype) [M, E], row stride ldl elements (ldl >= E),
+ *                    aligned to its element
+ *   correction_bias  NULL or fp32 [E]
+ *   topk_ids int32 [M, topk], topk_weights fp32 [M, topk], contiguous
+ *   1 <= E <= 512, 1 <= topk <= 32, 1 <= n_group <= 64 dividing E, 1 <= topk_group <= n_group,
+ *   topk <= topk_group * (E / n_group), scale finite (else MXQ_ERR_SHAPE for E, MXQ_ERR_ARG).
+ *   0 <= M <= 2^25 (0: no-op). */
+#define MXQ_SCORE_SOFTMAX 0
+#define MXQ_SCORE_SIGMOID 1
+#define MXQ_GROUP_MAX 0
+#define MXQ_GROUP_TOP2 1
+typedef struct mxq_moe_router {
+  int32_t topk;
+  int32_t scoring;
+  int32_t n_group;
+  int32_t topk_group;
+  int32_t group_score;
+  int32_t renormalize;
+  float scale;
+} mxq_moe_router;
+mxq_status mxq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int32_t E, int64_t ldl,
+                         const mxq_moe_router* router, const float* correction_bias, int32_t* topk_ids,
+                         float* topk_weights, void* stream);
+
+/* ------------------------------------------------------------------ whole MoE layer, few tokens
+ * Router product, routing, expert products and combine of at most 16 tokens in one call:
+ *   logits = x @ gate^T + gate_bias            (fp32 sums)
+ *   (ids, w) = the routing above
+ *   g, u = x[t] @ w1[e]^T + w1_bias[e]  (rows [0, I) of w1 the gate, [I, 2I) the up projection)
+ *   out[t] = bf16( sum_j (w[t, j] * silu(g) * u) @ w2[ids[t, j]]^T )
+ * Weights, scales, bias and layouts are those of mxq_fused_moe_fp8 (with bf16 activations) and
+ * mxq_fused_moe_mxfp4.  The arithmetic keeps more than theirs: nothing is rounded before
+ * w * silu(g) * u, which is kept as two bf16 terms (17 significant bits), so outputs agree with
+ * route + fused MoE within the fused MoE's rounding.  Both layouts give bit-identical outputs.
+ *   x          bf16 [M, H], row stride ldx elements (ldx >= H, multiple of 8); 0 <= M <= 16 (0: no-op)
+ *   gate       [E, H] contiguous, bf16 or fp32 (gate_dtype); gate_bias NULL or fp32 [E]
+ *   out        bf16 [M, H], row stride ldo elements (ldo >= H); a token without a live expert gets zeros
+ *   workspace  mxq_moe_layer_workspace_size(M, H, I, E, topk, weights) bytes (0: sizes the layer does
+ *              not take), contents arbitrary; concurrent calls need workspaces of their own
+ *   H and I multiples of 128 (FP8) or 32 (MXFP4); E <= 512; the rows of one token have to fit the
+ *   GPU's on-chip memory (H up to about 70000, I up to about 18000), else MXQ_ERR_SHAPE.  Experts
+ *   that no token chose are never read. */
+size_t mxq_moe_layer_workspace_size(int64_t M, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t weights);
+mxq_status mxq_moe_layer_fp8(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx, const void* gate,
+                             int32_t gate_dtype, const float* gate_bias, const mxq_moe_router* router,
+                             const float* correction_bias, const void* w1, const float* w1_scale, const void* w2,
+                             const float* w2_scale, const float* w1_bias, int32_t weight_layout, void* out,
+                             int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+mxq_status mxq_moe_layer_mxfp4(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx,
+                               const void* gate, int32_t gate_dtype, const float* gate_bias,
+                               const mxq_moe_router* router, const float* correction_bias, const void* w1,
+                               const void* w1_scale, const void* w2, const void* w2_scale, const float* w1_bias,
+                               int32_t weight_layout, void* out, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ 4-bit weights with group scales
+ * out[m, n] = bf16( sum_g s[n, g] * sum_{k in group g} x[m, k] * (q[n, k] - z[n, g]) + bias[n] )
+ *   A        bf16 [M, K], row stride lda elements (lda >= K, multiple of 8)
+ *   W        unsigned 4-bit codes [N, K/2], contiguous, element 2j in the low nibble of byte j
+ *   group    32, 64 or 128 elements of a row share a scale (else MXQ_ERR_BLOCK); K % group == 0
+ *   w_scale  [N, K/group] of scale_dtype (MXQ_DTYPE_F32 or MXQ_DTYPE_BF16), contiguous
+ *   w_zero   NULL (z = 8), or 4-bit zero points [N, ceil(K/group/2)], contiguous, group 2j in the
+ *            low nibble of byte j
+ *   bias     NULL or [N] of bias_dtype (fp32 or bf16), added in fp32
+ *   out      bf16 [M, N], row stride ldo elements (ldo >= N)
+ *   workspace mxq_int4_linear_workspace_size(M, N, K) bytes (NULL allowed where it is 0): the fp32
+ *            partial sums of a K split (added in chunk order; at most 16 MiB)
+ *   fp32 sums; the scales multiply fp32 group sums, so the weights themselves are never rounded.
+ *   w_scale, w_zero, bias and out need only their element's alignment.
+ *   M <= 2^19, N and K <= 2^28; M == 0 or N == 0: no-op. */
+size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+mxq_status mxq_int4_linear(const void* A, int64_t M, int64_t K, int64_t lda, const void* W, int64_t N, int32_t group,
+                           const void* w_scale, int32_t scale_dtype, const void* w_zero, const void* bias,
+                           int32_t bias_dtype, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 
 #ifdef __cplusplus

@@ -23,6 +23,12 @@ from .ops import (  # noqa: F401
     fused_moe_workspace_layout,
     silu_and_mul,
     Dispatch,
+    Router,
+    moe_route,
+    moe_layer_fp8,
+    moe_layer_mxfp4,
+    moe_layer_workspace,
+    int4_linear,
 )
 from ._lib import (  # noqa: F401
     LIB_PATH,
@@ -38,4 +44,10 @@ from ._lib import (  # noqa: F401
     MXQ_SORT_ALWAYS,
     MXQ_FUSE_AUTO,
     MXQ_FUSE_NONE,
+    MXQ_WEIGHTS_FP8_BLOCK,
+    MXQ_WEIGHTS_MXFP4,
+    MXQ_SCORE_SOFTMAX,
+    MXQ_SCORE_SIGMOID,
+    MXQ_GROUP_MAX,
+    MXQ_GROUP_TOP2,
 )

@@ -48,6 +48,11 @@ MXQ_FUSE_NONE = 1
 MXQ_LAYOUT_PLAIN = 0
 MXQ_LAYOUT_TILED = 1
 
+MXQ_SCORE_SOFTMAX = 0
+MXQ_SCORE_SIGMOID = 1
+MXQ_GROUP_MAX = 0
+MXQ_GROUP_TOP2 = 1
+
 # fields of mxq_fused_moe_plan, and the values of its enumerated fields
 MOE_PLAN_FIELDS = ("path", "tiles", "classes", "block_m1", "block_m2", "k_split1", "k_split2", "silu", "combine")
 MOE_PLAN_NAMES = {
@@ -67,6 +72,13 @@ class MoeDispatch(C.Structure):
     _fields_ = [("mode", C.c_int32), ("forced_class", C.c_int32), ("tiny_max_rows", C.c_int32),
                 ("tiny_kernel", C.c_int32), ("k_split", C.c_int32), ("sort", C.c_int32),
                 ("fuse", C.c_int32)]
+
+
+class MoeRouter(C.Structure):
+    """struct mxq_moe_router (how a token's experts are chosen)."""
+    _fields_ = [("topk", C.c_int32), ("scoring", C.c_int32), ("n_group", C.c_int32), ("topk_group", C.c_int32),
+                ("group_score", C.c_int32), ("renormalize", C.c_int32), ("scale", C.c_float)]
+
 
 _p = C.c_void_p
 _i32 = C.c_int32
@@ -106,6 +118,15 @@ SIGNATURES = {
     "mxq_moe_prepack_scales_size": (_sz, [_i64, _i64, _i64]),
     "mxq_moe_prepack": (_i32, [_p, _i64, _i64, _i64, _p, _p]),
     "mxq_moe_prepack_scales": (_i32, [_p, _i64, _i64, _i64, _p, _p]),
+    "mxq_moe_route": (_i32, [_p, _i32, _i64, _i32, _i64, C.POINTER(MoeRouter), _p, _p, _p, _p]),
+    "mxq_moe_layer_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
+    "mxq_moe_layer_fp8": (_i32, [_p, _i64, _i64, _i64, _i32, _i64, _p, _i32, _p, C.POINTER(MoeRouter), _p, _p, _p,
+                                  _p, _p, _p, _i32, _p, _i64, _p, _sz, _p]),
+    "mxq_moe_layer_mxfp4": (_i32, [_p, _i64, _i64, _i64, _i32, _i64, _p, _i32, _p, C.POINTER(MoeRouter), _p, _p, _p,
+                                    _p, _p, _p, _i32, _p, _i64, _p, _sz, _p]),
+    "mxq_int4_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "mxq_int4_linear": (_i32, [_p, _i64, _i64, _i64, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _p, _i64, _p, _sz,
+                                _p]),
 }
 
 _lock = threading.Lock()

@@ -883,6 +883,104 @@ size_t mx_quant_bytes(int64_t M, int64_t K, int32_t a_dtype) {
   return align256(size_t(M) * K) + align256(size_t(M) * (K / 32));
 }
 
+// ---------------------------------------------------------------- routing, few-token layer
+
+// Checks a router and fills the kernels' arguments.
+mxq_status read_router(const mxq_moe_router* r, int32_t E, const float* correction_bias, RouteArgs& a) {
+  if (E < 1 || E > kRouteMaxExperts) return MXQ_ERR_SHAPE;
+  if (!r) return MXQ_ERR_NULL;
+  if (r->scoring != MXQ_SCORE_SOFTMAX && r->scoring != MXQ_SCORE_SIGMOID) return MXQ_ERR_ARG;
+  if (r->group_score != MXQ_GROUP_MAX && r->group_score != MXQ_GROUP_TOP2) return MXQ_ERR_ARG;
+  if (r->renormalize != 0 && r->renormalize != 1) return MXQ_ERR_ARG;
+  if (r->n_group < 1 || r->n_group > kRouteMaxGroups || E % r->n_group != 0) return MXQ_ERR_ARG;
+  if (r->topk_group < 1 || r->topk_group > r->n_group) return MXQ_ERR_ARG;
+  if (r->topk < 1 || r->topk > kRouteMaxTopk || r->topk > r->topk_group * (E / r->n_group)) return MXQ_ERR_ARG;
+  if (!(r->scale - r->scale == 0.f)) return MXQ_ERR_ARG;  // NaN or infinite
+  a.E = E;
+  a.topk = r->topk;
+  a.sigmoid = r->scoring == MXQ_SCORE_SIGMOID;
+  a.n_group = r->n_group;
+  a.topk_group = r->topk_group;
+  a.group_top2 = r->group_score == MXQ_GROUP_TOP2;
+  a.renormalize = r->renormalize;
+  a.scale = r->scale;
+  a.bias = correction_bias;
+  a.group_size = E / r->n_group;
+  a.group_magic = uint32_t(((1 << 20) + a.group_size - 1) / a.group_size);
+  return MXQ_OK;
+}
+
+// Regions of the few-token layer's workspace.
+struct LayerWs {
+  size_t part, h, total;
+  int32_t S, chunk, pass;
+};
+
+// false: sizes the layer does not take
+bool layer_ws(int64_t M, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t weights, LayerWs& w) {
+  const int64_t unit = weights == MXQ_WEIGHTS_FP8_BLOCK ? 128 : 32;
+  if (weights != MXQ_WEIGHTS_FP8_BLOCK && weights != MXQ_WEIGHTS_MXFP4) return false;
+  if (M < 1 || M > kLayerMaxTokens || H < unit || I < unit || H % unit != 0 || I % unit != 0) return false;
+  if (E < 1 || E > kRouteMaxExperts || topk < 1 || topk > kRouteMaxTopk || topk > E) return false;
+  // one expert's weights are addressed with 32-bit byte offsets (rows padded to 256 elements)
+  constexpr int64_t k4G = int64_t(1) << 32;
+  if (H > (1 << 20) || I > (1 << 20) || 2 * I * (H + 256) >= k4G || H * (I + 256) >= k4G) return false;
+  const int wfmt = weights == MXQ_WEIGHTS_MXFP4 ? W_E2M1_MX : W_E4M3_BLOCK;
+  w.pass = layer_pass_tokens(wfmt, H, E, topk);
+  if (w.pass < 1) return false;
+  w.pass = int32_t(std::min<int64_t>(w.pass, M));
+  if (layer_batch_rows(wfmt, I, E, w.pass * topk) < 1) return false;
+  layer_gate_split(E, H, w.S, w.chunk);
+  w.part = 0;
+  w.h = align256(size_t(w.S) * size_t(M) * size_t(E) * 4);
+  w.total = w.h + align256(size_t(w.pass) * size_t(topk) * 2 * size_t(I) * 2);
+  return true;
+}
+
+mxq_status run_layer(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx, const void* gate,
+                     int32_t gate_dtype, const float* gate_bias, const mxq_moe_router* router,
+                     const float* correction_bias, const void* w1, const void* w1_scale, const void* w2,
+                     const void* w2_scale, const float* w1_bias, int32_t weight_layout, void* out, int64_t ldo,
+                     void* workspace, size_t workspace_bytes, int32_t weights, void* stream) {
+  if (gate_dtype != MXQ_DTYPE_BF16 && gate_dtype != MXQ_DTYPE_F32) return MXQ_ERR_DTYPE;
+  if (weight_layout != MXQ_LAYOUT_PLAIN && weight_layout != MXQ_LAYOUT_TILED) return MXQ_ERR_ARG;
+  LayerArgs a{};
+  MXQ_TRY(read_router(router, E, correction_bias, a.rt));
+  if (M == 0) return MXQ_OK;
+  LayerWs ws;
+  if (!layer_ws(M, H, I, E, router->topk, weights, ws)) return MXQ_ERR_SHAPE;
+  if (ldx < H || ldx % 8 != 0 || ldo < H) return MXQ_ERR_SHAPE;
+  if (!x || !gate || !w1 || !w1_scale || !w2 || !w2_scale || !out) return MXQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(gate) || !aligned16(w1) || !aligned16(w2)) return MXQ_ERR_SHAPE;
+  if (!workspace || workspace_bytes < ws.total) return MXQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MXQ_ERR_SHAPE;
+  MXQ_TRY(check_arch());
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.H = H;
+  a.I = I;
+  a.M_all = int32_t(M);
+  a.gate = gate;
+  a.gate_f32 = gate_dtype == MXQ_DTYPE_F32;
+  a.gate_bias = gate_bias;
+  a.wfmt = weights == MXQ_WEIGHTS_MXFP4 ? W_E2M1_MX : W_E4M3_BLOCK;
+  a.tiled = weight_layout == MXQ_LAYOUT_TILED;
+  a.w1 = static_cast<const uint8_t*>(w1);
+  a.s1 = static_cast<const uint8_t*>(w1_scale);
+  a.w2 = static_cast<const uint8_t*>(w2);
+  a.s2 = static_cast<const uint8_t*>(w2_scale);
+  a.b1 = w1_bias;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  a.part = reinterpret_cast<float*>(base + ws.part);
+  a.S = ws.S;
+  a.chunk = ws.chunk;
+  a.h = reinterpret_cast<uint16_t*>(base + ws.h);
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  launch_moe_layer(a, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -1453,6 +1551,89 @@ mxq_status mxq_moe_prepack_scales(const void* s, int64_t E, int64_t N, int64_t g
   MXQ_TRY(check_arch());
   launch_prepack_s(static_cast<const uint8_t*>(s), E, N, groups, static_cast<uint8_t*>(out),
                    static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+mxq_status mxq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, int32_t E, int64_t ldl,
+                         const mxq_moe_router* router, const float* correction_bias, int32_t* topk_ids,
+                         float* topk_weights, void* stream) {
+  if (logits_dtype != MXQ_DTYPE_F32 && logits_dtype != MXQ_DTYPE_BF16) return MXQ_ERR_DTYPE;
+  RouteArgs a{};
+  MXQ_TRY(read_router(router, E, correction_bias, a));
+  if (M < 0 || M > (int64_t(1) << 25) || ldl < E) return MXQ_ERR_SHAPE;  // one launch of 64 M threads
+  if (M == 0) return MXQ_OK;
+  if (!logits || !topk_ids || !topk_weights) return MXQ_ERR_NULL;
+  const uintptr_t align = logits_dtype == MXQ_DTYPE_F32 ? 3u : 1u;
+  if (reinterpret_cast<uintptr_t>(logits) & align) return MXQ_ERR_SHAPE;
+  MXQ_TRY(check_arch());
+  launch_moe_route(logits, logits_dtype == MXQ_DTYPE_BF16, M, ldl, a, topk_ids, topk_weights,
+                   static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+size_t mxq_moe_layer_workspace_size(int64_t M, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t weights) {
+  LayerWs w;
+  return layer_ws(M, H, I, E, topk, weights, w) ? w.total : 0;
+}
+
+mxq_status mxq_moe_layer_fp8(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx, const void* gate,
+                             int32_t gate_dtype, const float* gate_bias, const mxq_moe_router* router,
+                             const float* correction_bias, const void* w1, const float* w1_scale, const void* w2,
+                             const float* w2_scale, const float* w1_bias, int32_t weight_layout, void* out,
+                             int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_layer(x, M, H, I, E, ldx, gate, gate_dtype, gate_bias, router, correction_bias, w1, w1_scale, w2,
+                   w2_scale, w1_bias, weight_layout, out, ldo, workspace, workspace_bytes, MXQ_WEIGHTS_FP8_BLOCK,
+                   stream);
+}
+
+mxq_status mxq_moe_layer_mxfp4(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx,
+                               const void* gate, int32_t gate_dtype, const float* gate_bias,
+                               const mxq_moe_router* router, const float* correction_bias, const void* w1,
+                               const void* w1_scale, const void* w2, const void* w2_scale, const float* w1_bias,
+                               int32_t weight_layout, void* out, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_layer(x, M, H, I, E, ldx, gate, gate_dtype, gate_bias, router, correction_bias, w1, w1_scale, w2,
+                   w2_scale, w1_bias, weight_layout, out, ldo, workspace, workspace_bytes, MXQ_WEIGHTS_MXFP4, stream);
+}
+
+size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return int4_plan(M, N, K).partial_bytes;
+}
+
+mxq_status mxq_int4_linear(const void* A, int64_t M, int64_t K, int64_t lda, const void* W, int64_t N, int32_t group,
+                           const void* w_scale, int32_t scale_dtype, const void* w_zero, const void* bias,
+                           int32_t bias_dtype, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (group != 32 && group != 64 && group != 128) return MXQ_ERR_BLOCK;
+  if (scale_dtype != MXQ_DTYPE_F32 && scale_dtype != MXQ_DTYPE_BF16) return MXQ_ERR_DTYPE;
+  if (bias && bias_dtype != MXQ_DTYPE_F32 && bias_dtype != MXQ_DTYPE_BF16) return MXQ_ERR_DTYPE;
+  if (M < 0 || N < 0 || K < 0 || K % group != 0 || lda < K || lda % 8 != 0 || ldo < N) return MXQ_ERR_SHAPE;
+  // row tiles on the grid's second dimension, 4 N threads on its first, a row's elements in 32 bits
+  if (M > (int64_t(1) << 19) || N > (int64_t(1) << 28) || K > (int64_t(1) << 28)) return MXQ_ERR_SHAPE;
+  if (M == 0 || N == 0) return MXQ_OK;
+  if (K == 0) return MXQ_ERR_SHAPE;
+  if (!A || !W || !w_scale || !out) return MXQ_ERR_NULL;
+  if (!aligned16(A) || !aligned16(W)) return MXQ_ERR_SHAPE;
+  const size_t need = mxq_int4_linear_workspace_size(M, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return MXQ_ERR_SHAPE;
+  MXQ_TRY(check_arch());
+  Int4Args a{};
+  a.A = A;
+  a.lda = lda;
+  a.W = static_cast<const uint8_t*>(W);
+  a.s = w_scale;
+  a.s_bf16 = scale_dtype == MXQ_DTYPE_BF16;
+  a.z = static_cast<const uint8_t*>(w_zero);
+  a.bias = bias;
+  a.bias_bf16 = bias_dtype == MXQ_DTYPE_BF16;
+  a.out = out;
+  a.ldo = ldo;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  launch_int4_linear(a, group, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
   return launch_status();
 }
 

@@ -527,3 +527,220 @@ def fused_moe_mxfp4(x, topk_ids, topk_weights, w1, w1_scale, w2, w2_scale, w1_bi
                                       workspace.numel(), _stream())
     L.check("mxq_fused_moe_mxfp4", st)
     return out
+
+
+# ----------------------------------------------------------------------- routing, few-token layer
+
+_SCORING = {"softmax": L.MXQ_SCORE_SOFTMAX, "sigmoid": L.MXQ_SCORE_SIGMOID}
+_GROUP_SCORE = {"max": L.MXQ_GROUP_MAX, "top2": L.MXQ_GROUP_TOP2}
+
+
+class Router(NamedTuple):
+    """How a token's experts are chosen (``struct mxq_moe_router``): ``topk`` experts by their
+    ``scoring`` ("softmax" or "sigmoid") plus the correction bias, among the ``topk_group`` best of
+    ``n_group`` groups (by "max" or "top2" ``group_score``), their scores renormalised over the
+    chosen ones or not, times ``scale``."""
+    topk: int
+    scoring: str = "softmax"
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: str = "max"
+    renormalize: bool = False
+    scale: float = 1.0
+
+
+def _router(r: Router):
+    if not isinstance(r, Router):
+        raise ValueError(f"router must be a Router, got {type(r).__name__}")
+    if r.scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {r.scoring!r}")
+    if r.group_score not in _GROUP_SCORE:
+        raise ValueError(f"group_score must be 'max' or 'top2', got {r.group_score!r}")
+    return ctypes.byref(L.MoeRouter(int(r.topk), _SCORING[r.scoring], int(r.n_group), int(r.topk_group),
+                                    _GROUP_SCORE[r.group_score], int(bool(r.renormalize)), float(r.scale)))
+
+
+def _one_device(x: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
+    """Every tensor on x's GPU, and that GPU the current one (kernels run on its current stream)."""
+    if not x.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    for t in ts:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"all tensors must be on {x.device}, got one on {t.device}")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _vector(t: Optional[torch.Tensor], n: int, name: str) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != n:
+        raise ValueError(f"{name} must be fp32 with {n} elements")
+    return t.contiguous()
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """2-D rows as the kernels read them: unit last stride, 16-byte aligned, no two rows overlapping."""
+    t = _unit_last(t)
+    return t.contiguous() if t.shape[0] > 1 and t.stride(0) < t.shape[1] else t
+
+
+_LOGITS = {torch.float32: L.MXQ_DTYPE_F32, torch.bfloat16: L.MXQ_DTYPE_BF16}
+
+
+def moe_route(logits: torch.Tensor, router: Router, correction_bias: Optional[torch.Tensor] = None
+              ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Router logits fp32 or bf16 [M, E] -> (topk_ids int32 [M, topk], topk_weights fp32 [M, topk])
+    as :func:`fused_moe_fp8` and :func:`fused_moe_mxfp4` take them (``mxq_moe_route``): largest pick
+    first, equal picks by the lower expert; NaN and -inf logits take their expert out, and a slot
+    without an expert gets id -1 and weight 0."""
+    if logits.dtype not in _LOGITS or logits.dim() != 2:
+        raise ValueError("logits must be fp32 or bf16 [M, E]")
+    M, E = logits.shape
+    r = _router(router)
+    bias = _vector(correction_bias, E, "correction_bias")
+    _one_device(logits, bias)
+    if logits.stride(1) != 1 or (M > 1 and logits.stride(0) < E):
+        logits = logits.contiguous()
+    ids = torch.empty((M, router.topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((M, router.topk), dtype=torch.float32, device=logits.device)
+    st = L.load().mxq_moe_route(logits.data_ptr(), _LOGITS[logits.dtype], M, E, max(logits.stride(0), E), r,
+                                _ptr(bias), ids.data_ptr(), weights.data_ptr(), _stream())
+    L.check("mxq_moe_route", st)
+    return ids, weights
+
+
+def moe_layer_workspace(M: int, H: int, I: int, E: int, topk: int, weights: int, device) -> torch.Tensor:
+    """Workspace of a ``moe_layer_*`` call (``weights``: MXQ_WEIGHTS_*); its contents do not matter."""
+    n = L.load().mxq_moe_layer_workspace_size(M, H, I, E, topk, weights)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _moe_layer(name, weights, x, gate, router, w1, s1, w2, s2, w1_bias, gate_bias, correction_bias, workspace, out,
+               layout, rb1, rb2, shape_s1, shape_s2):
+    M, H = x.shape
+    E, two_i, h1 = w1.shape
+    I = two_i // 2
+    r = _router(router)
+    if gate.dtype not in _LOGITS or tuple(gate.shape) != (E, H):
+        raise ValueError(f"gate must be fp32 or bf16 [{E}, {H}]")
+    if two_i % 2 or h1 != rb1 or tuple(w2.shape) != (E, H, rb2):
+        raise ValueError(f"w1 must be [E, 2I, {rb1}] and w2 [E, H, {rb2}] in this layout")
+    if tuple(s1.shape) != shape_s1 or tuple(s2.shape) != shape_s2:
+        raise ValueError(f"scales must be {list(shape_s1)} and {list(shape_s2)} in this layout")
+    if M > 16:
+        raise ValueError(f"at most 16 tokens, got {M}: moe_route and the fused MoE take more")
+    b1 = _vector(w1_bias, E * two_i, "w1_bias")
+    gb = _vector(gate_bias, E, "gate_bias")
+    cb = _vector(correction_bias, E, "correction_bias")
+    _one_device(x, gate, w1, s1, w2, s2, b1, gb, cb, workspace, out)
+    x = _rows(x)
+    gate = gate.contiguous()
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, H) or out.stride(1) != 1 or (M > 1 and out.stride(0) < H):
+        raise ValueError(f"out must be bf16 [{M}, {H}] with whole rows")
+    if workspace is None:
+        workspace = moe_layer_workspace(M, H, I, E, router.topk, weights, x.device)
+    st = getattr(L.load(), name)(x.data_ptr(), M, H, I, E, max(x.stride(0), H), gate.data_ptr(), _LOGITS[gate.dtype],
+                                 _ptr(gb), r, _ptr(cb), w1.data_ptr(), s1.data_ptr(), w2.data_ptr(), s2.data_ptr(),
+                                 _ptr(b1), layout, out.data_ptr(), max(out.stride(0), H), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream())
+    L.check(name, st)
+    return out
+
+
+def moe_layer_fp8(x: torch.Tensor, gate: torch.Tensor, router: Router, w1: torch.Tensor, w1_scale: torch.Tensor,
+                  w2: torch.Tensor, w2_scale: torch.Tensor, w1_bias: Optional[torch.Tensor] = None,
+                  gate_bias: Optional[torch.Tensor] = None, correction_bias: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  weight_layout: str = "plain") -> torch.Tensor:
+    """A whole MoE layer with block-FP8 experts for at most 16 tokens -> bf16 [M, H]: router product
+    with ``gate`` (bf16 or fp32 [E, H]), routing as :func:`moe_route`, expert products with the
+    weights of :func:`fused_moe_fp8`, weighted sum."""
+    layout = _layout(weight_layout)
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError("x must be bf16 [M, H]")
+    w1 = _as_u8(w1, "w1").contiguous()
+    w2 = _as_u8(w2, "w2").contiguous()
+    if w1_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
+        raise ValueError("block scales must be fp32")
+    if w1.dim() != 3:
+        raise ValueError("w1 must be [E, 2I, row bytes]")
+    H, E, I = x.shape[1], w1.shape[0], w1.shape[1] // 2
+    if H % 128 or I % 128:
+        raise ValueError(f"H ({H}) and I ({I}) must be multiples of 128")
+    return _moe_layer("mxq_moe_layer_fp8", L.MXQ_WEIGHTS_FP8_BLOCK, x, gate, router, w1, w1_scale.contiguous(), w2,
+                      w2_scale.contiguous(), w1_bias, gate_bias, correction_bias, workspace, out, layout, H, I,
+                      (E, -(-2 * I // 128), H // 128), (E, -(-H // 128), I // 128))
+
+
+def moe_layer_mxfp4(x: torch.Tensor, gate: torch.Tensor, router: Router, w1: torch.Tensor, w1_scale: torch.Tensor,
+                    w2: torch.Tensor, w2_scale: torch.Tensor, w1_bias: Optional[torch.Tensor] = None,
+                    gate_bias: Optional[torch.Tensor] = None, correction_bias: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    weight_layout: str = "plain") -> torch.Tensor:
+    """A whole MoE layer with MXFP4 experts for at most 16 tokens -> bf16 [M, H]: as
+    :func:`moe_layer_fp8`, with the weights of :func:`fused_moe_mxfp4`."""
+    layout = _layout(weight_layout)
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError("x must be bf16 [M, H]")
+    for t, n in ((w1, "w1"), (w2, "w2"), (w1_scale, "w1_scale"), (w2_scale, "w2_scale")):
+        if t.dtype != torch.uint8:
+            raise ValueError(f"{n} must be uint8")
+    if w1.dim() != 3:
+        raise ValueError("w1 must be [E, 2I, row bytes]")
+    H, E, I = x.shape[1], w1.shape[0], w1.shape[1] // 2
+    if H % 32 or I % 32:
+        raise ValueError(f"H ({H}) and I ({I}) must be multiples of 32")
+    if layout == L.MXQ_LAYOUT_PLAIN:
+        rb1, rb2, g1, g2 = H // 2, I // 2, H // 32, I // 32
+    else:
+        rb1, rb2 = _tiled_row(H // 2), _tiled_row(I // 2)
+        g1, g2 = -(-(H // 32) // 8) * 8, -(-(I // 32) // 8) * 8
+    return _moe_layer("mxq_moe_layer_mxfp4", L.MXQ_WEIGHTS_MXFP4, x, gate, router, w1.contiguous(),
+                      w1_scale.contiguous(), w2.contiguous(), w2_scale.contiguous(), w1_bias, gate_bias,
+                      correction_bias, workspace, out, layout, rb1, rb2, (E, 2 * I, g1), (E, H, g2))
+
+
+# ----------------------------------------------------------------------- 4-bit weights, group scales
+
+def int4_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
+                weight_zero: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """4-bit linear with group scales: bf16 [..., K] @ ((q - z) * s)^T (+ bias) -> bf16 [..., N].
+
+    ``weight``: unsigned 4-bit codes, packed uint8 [N, K/2] (element 2j in the low nibble of byte
+    j).  ``weight_scale``: fp32 or bf16 [N, K/group], group 32, 64 or 128 (taken from its shape).
+    ``weight_zero``: None (z = 8) or packed 4-bit zero points uint8 [N, ceil(K/group/2)]."""
+    if x.dtype != torch.bfloat16:
+        raise ValueError("x must be bf16")
+    if weight.dtype != torch.uint8 or weight.dim() != 2:
+        raise ValueError("weight must be packed uint8 [N, K/2]")
+    N, K = weight.shape[0], weight.shape[1] * 2
+    if x.dim() < 1 or x.shape[-1] != K:
+        raise ValueError(f"weight K {K} != input K {x.shape[-1] if x.dim() else None}")
+    if weight_scale.dtype not in _LOGITS or weight_scale.dim() != 2 or weight_scale.shape[0] != N:
+        raise ValueError(f"weight_scale must be fp32 or bf16 [{N}, K/group]")
+    groups = weight_scale.shape[1]
+    if groups == 0 or K % groups or K // groups not in (32, 64, 128):
+        raise ValueError(f"weight_scale has {groups} groups for K {K}: the group must be 32, 64 or 128")
+    if weight_zero is not None and (weight_zero.dtype != torch.uint8 or
+                                    tuple(weight_zero.shape) != (N, -(-groups // 2))):
+        raise ValueError(f"weight_zero must be packed uint8 [{N}, {-(-groups // 2)}]")
+    if bias is not None and bias.numel() != N:
+        raise ValueError("bias must have N elements")
+    _one_device(x, weight, weight_scale, weight_zero, bias)
+    x2 = _rows(x.reshape(-1, K))
+    M = x2.shape[0]
+    w, s = weight.contiguous(), weight_scale.contiguous()
+    z = None if weight_zero is None else weight_zero.contiguous()
+    b = None if bias is None else bias.contiguous()
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    lib = L.load()
+    ws_bytes = lib.mxq_int4_linear_workspace_size(M, N, K)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
+    st = lib.mxq_int4_linear(x2.data_ptr(), M, K, max(x2.stride(0), K), w.data_ptr(), N, K // groups, s.data_ptr(),
+                             _LOGITS[s.dtype], _ptr(z), _ptr(b), _bias_dtype(b), out.data_ptr(), N, _ptr(ws), ws_bytes,
+                             _stream())
+    L.check("mxq_int4_linear", st)
+    return out.view(*x.shape[:-1], N)

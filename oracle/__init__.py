@@ -28,6 +28,9 @@ Modules:
 * ``moe``     -- routed fused-MoE experts (FP8 block and MXFP4 weights).
 * ``mx``      -- MXFP8 quantisation (e4m3 + e8m0 per 32) and the MX-scaled linear
   (MXFP8 activations x MXFP8 / MXFP4 weights).
+* ``route``   -- router logits to experts and weights, one token at a time.
+* ``layer``   -- a whole MoE layer of a few tokens, with a bound on fp32 differences.
+* ``int4``    -- linear with 4-bit weights and group scales.
 
 Every function has at least one pin in ``tests/test_oracle_*.py`` that checks
 it against something other than itself (library routines, closed forms,
@@ -35,4 +38,4 @@ brute force, invariants).  The one unpinned piece is the exponential inside
 SiLU (host libm vs device math): only the bf16 tolerance covers it.
 """
 
-from . import codecs, quant, dense, align, moe, mx  # noqa: F401
+from . import codecs, quant, dense, align, moe, mx, route, layer, int4  # noqa: F401

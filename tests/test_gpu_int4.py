@@ -1,0 +1,153 @@
+"""mxq_int4_linear against the float64 oracle.
+
+Exactness: with integer activations of magnitude at most 4, scales that are powers of two and
+K <= 2048 every intermediate is a multiple of 2^-3 below 2^24 * 2^-3 (4 * 143 * 2048 < 2^21), so fp32
+sums in any order are exact and the output has to be the bf16 rounding of the exact value, bit for bit.
+
+Random data: the only rounding besides fp32's is the last one, at most half a bf16 step (2^-8
+relative).  A group's sum of x (128 + q) and its correction (128 + z) X have magnitudes of at most
+143 sum |x|, each carries at most (G + 4) roundings of 2^-24, and the K / G scaled group sums are
+added with as many more: E = (G + K/G + 16) 2^-24 * 286 * sum |x s|.  That worst case is loose, so
+the whole output is also held to 2^-8 of its norm (the fp32 part, random in sign, is far below).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_block_scaled_expert_amd import _lib as L
+from mxfp4_block_scaled_expert_amd import ops
+from oracle.int4 import int4_linear
+from tests._util import gpu
+
+pytestmark = pytest.mark.gpu
+HALF = torch.finfo(torch.bfloat16).eps / 2
+
+
+def _weights(N, K, G, seed, zero=True, sdtype=torch.float32, pow2=False):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    z = torch.randint(0, 256, (N, -(-(K // G) // 2)), generator=g, dtype=torch.uint8) if zero else None
+    s = torch.exp2(torch.randint(-3, 1, (N, K // G), generator=g).float()) if pow2 else \
+        (0.5 + torch.rand(N, K // G, generator=g)) * 0.01
+    return w, s.to(sdtype), z
+
+
+def _run(x, w, s, z, b=None):
+    d = gpu()
+    out = ops.int4_linear(x.to(d), w.to(d), s.to(d), None if z is None else z.to(d), None if b is None else b.to(d))
+    torch.cuda.synchronize()
+    return out.cpu()
+
+
+def _oracle(x, w, s, z, G, b=None):
+    return int4_linear(x.double().numpy(), w.numpy(), s.double().numpy(), None if z is None else z.numpy(), G,
+                       None if b is None else b.double().numpy())
+
+
+def _check_random(x, w, s, z, G, b=None):
+    out = _run(x, w, s, z, b).double().numpy()
+    want = _oracle(x, w, s, z, G, b)
+    K = x.shape[1]
+    mag = np.abs(x.double().numpy()) @ np.repeat(np.abs(s.double().numpy()), G, axis=1).T
+    bound = HALF * np.abs(want) * (1 + HALF) + (G + K / G + 16) * 2.0 ** -24 * 286 * mag
+    assert (np.abs(out - want) <= bound).all()
+    assert np.linalg.norm(out - want) <= HALF * np.linalg.norm(want)
+
+
+SHAPES = [(1, 1, 128), (1, 16, 128), (1, 17, 256), (2, 70, 384), (3, 130, 1024), (4, 33, 2048), (5, 64, 512),
+          (7, 96, 640), (8, 257, 896), (13, 40, 1152), (16, 129, 2048), (17, 65, 256), (31, 128, 1024),
+          (63, 200, 384), (64, 64, 128), (65, 31, 512), (100, 300, 1664), (128, 128, 2048), (129, 257, 640)]
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_exact_sums_bit_for_bit(M, N, K, G):
+    # K down to a multiple of the group that is none of the 128-wide step where the group allows it
+    K = K if G == 128 else K - (G if (M + N) % 2 else 0)
+    g = torch.Generator().manual_seed(M * 7 + N)
+    x = torch.randint(-4, 5, (M, K), generator=g).to(torch.bfloat16)
+    for zero, sdtype in ((True, torch.float32), (False, torch.bfloat16)):
+        w, s, z = _weights(N, K, G, N + K, zero, sdtype, pow2=True)
+        b = torch.randint(-8, 9, (N,), generator=g).to(sdtype) if zero else None
+        out = _run(x, w, s, z, b)
+        want = torch.from_numpy(_oracle(x, w, s, z, G, b)).to(torch.bfloat16)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) or torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,N,K,G,zero,sdtype", [
+    (1, 7168, 2048, 128, False, torch.bfloat16), (3, 513, 4096, 64, True, torch.bfloat16),
+    (16, 300, 7168, 32, True, torch.float32), (97, 224, 576, 64, True, torch.float32),
+    (2, 48, 16384, 32, False, torch.float32), (1, 20, 32, 32, True, torch.float32),
+    (9, 64, 96, 32, True, torch.bfloat16), (64, 96, 8192, 128, True, torch.float32),
+    (300, 520, 1024, 128, True, torch.bfloat16), (513, 100, 192, 64, False, torch.float32)])
+def test_random_against_oracle(M, N, K, G, zero, sdtype):
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16)
+    w, s, z = _weights(N, K, G, K + N, zero, sdtype)
+    _check_random(x, w, s, z, G, torch.randn(N, generator=g) if N % 2 else None)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes(seed):
+    r = np.random.default_rng(seed)
+    G = int(r.choice([32, 64, 128]))
+    K = G * int(r.integers(1, max(2, 3000 // G)))
+    M = int(np.exp(r.uniform(0, np.log(200))))
+    N = int(np.exp(r.uniform(0, np.log(900))))
+    g = torch.Generator().manual_seed(seed)
+    w, s, z = _weights(N, K, G, seed, bool(r.integers(2)), torch.bfloat16 if r.integers(2) else torch.float32)
+    bias = [None, torch.randn(N, generator=g), torch.randn(N, generator=g).to(torch.bfloat16)][int(r.integers(3))]
+    _check_random(torch.randn(M, K, generator=g).to(torch.bfloat16), w, s, z, G, bias)
+
+
+def test_rows_do_not_depend_on_their_neighbours():
+    """A row's NaN, infinity or huge value stays in that row; a scale's in its column."""
+    M, N, K, G = 6, 48, 256, 64
+    x = torch.randn(M, K).to(torch.bfloat16)
+    w, s, z = _weights(N, K, G, 1)
+    base = _run(x, w, s, z)
+    for m_rows in (M, 2, 1):
+        y = x[:m_rows].clone()
+        y[0, 5] = float("nan")
+        if m_rows > 1:
+            y[1, 7] = float("inf")
+        t = s.clone()
+        t[9, 1] = float("nan")
+        out = _run(y, w, t, z)
+        assert out[0].isnan().all() and not out[1:2].isfinite().any()
+        keep = torch.arange(N) != 9
+        ref = _run(x[:m_rows], w, s, z)
+        assert torch.equal(out[2:][:, keep], ref[2:][:, keep]) and out[:, 9].isnan().all()
+    assert base.isfinite().all()
+
+
+def test_leading_dimensions_strides_and_empty():
+    w, s, z = (t.to(gpu()) for t in _weights(40, 128, 32, 3))
+    x = torch.randn(2, 3, 128, device=gpu()).to(torch.bfloat16)
+    out = ops.int4_linear(x, w, s, z)
+    assert out.shape == (2, 3, 40)
+    assert torch.equal(out.view(6, 40), ops.int4_linear(x.view(6, 128), w, s, z))
+    wide = torch.randn(6, 320, device=gpu()).to(torch.bfloat16)
+    for v in (wide[:, 64:192], wide[:, 3:131], wide[::2, :128], wide.t()[:128, :].t(), wide[:1, :128].expand(6, 128)):
+        assert torch.equal(ops.int4_linear(v, w, s, z), ops.int4_linear(v.contiguous(), w, s, z))
+    assert torch.equal(ops.int4_linear(x[0, 0], w, s, z), out[0, 0])
+    assert ops.int4_linear(x[:0], w, s, z).shape == (0, 3, 40)
+    assert ops.int4_linear(x, w[:0], s[:0], z[:0]).shape == (2, 3, 0)
+
+
+def test_output_stride_leaves_the_rest_alone():
+    lib = L.load()
+    for M, N, K in ((1, 33, 256), (5, 33, 256), (20, 33, 256), (3, 40, 8192)):
+        w, s, z = (t.to(gpu()) for t in _weights(N, K, 64, 4))
+        x = torch.randn(M, K, device=gpu()).to(torch.bfloat16)
+        out = torch.full((M + 1, N + 5), 3.0, dtype=torch.bfloat16, device=gpu())
+        n = lib.mxq_int4_linear_workspace_size(M, N, K)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=gpu())
+        st = lib.mxq_int4_linear(x.data_ptr(), M, K, K, w.data_ptr(), N, 64, s.data_ptr(), L.MXQ_DTYPE_F32, z.data_ptr(),
+                                 None, 0, out.data_ptr(), N + 5, ws.data_ptr(), n,
+                                 torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0
+        assert torch.equal(out[:M, :N], ops.int4_linear(x, w, s, z))
+        assert (out[M:] == 3).all() and (out[:, N:] == 3).all()

@@ -1,0 +1,155 @@
+"""mxq_moe_route against the float64 oracle: ids and their order exactly, weights within fp32.
+
+Tolerance of the weights: an fp32 exponential (2 ulp), a sum over at most 512 experts in a tree
+(9 roundings), a division and the scale, each 2^-24 relative, on both sides of the renormalising
+quotient: below 32 * 2^-24 = 2^-19.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_block_scaled_expert_amd import ops
+from oracle.route import route
+from tests._util import gpu
+
+pytestmark = pytest.mark.gpu
+RTOL = 2.0 ** -19
+
+
+def _check(logits, router, bias=None):
+    """logits: CPU tensor.  Runs the operator and compares."""
+    b = None if bias is None else bias.to(gpu())
+    ids, w = ops.moe_route(logits.to(gpu()), router, correction_bias=b)
+    torch.cuda.synchronize()
+    want_ids, want_w, _ = route(logits.double().numpy(), router.topk, sigmoid=router.scoring == "sigmoid",
+                                bias=None if bias is None else bias.double().numpy(), n_group=router.n_group,
+                                topk_group=router.topk_group, top2=router.group_score == "top2",
+                                renormalize=router.renormalize, scale=router.scale)
+    assert ids.dtype == torch.int32 and w.dtype == torch.float32
+    np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
+    np.testing.assert_allclose(w.double().cpu().numpy(), want_w, rtol=RTOL, atol=1e-37)
+    return ids, w
+
+
+def _logits(M, E, seed, dtype=torch.float32, std=2.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(M, E, generator=g) * std).to(dtype)
+
+
+R = ops.Router
+CASES = [
+    (1, 1, R(1)), (1, 2, R(2, renormalize=True)), (3, 5, R(5)), (1, 128, R(4, renormalize=True)),
+    (32, 128, R(4)), (33, 60, R(6, scoring="sigmoid")), (7, 64, R(8, renormalize=True, scale=2.5)),
+    (5, 65, R(3)), (9, 129, R(2, scoring="sigmoid", renormalize=True)), (6, 257, R(7)), (4, 511, R(32)),
+    (130, 512, R(8, renormalize=True)),
+    (17, 256, R(8, scoring="sigmoid", n_group=8, topk_group=4, group_score="top2", renormalize=True, scale=2.5)),
+    (17, 160, R(6, n_group=8, topk_group=3)), (8, 72, R(4, n_group=36, topk_group=5, group_score="top2")),
+    (8, 64, R(3, n_group=64, topk_group=3, group_score="top2")), (8, 512, R(8, n_group=2, topk_group=1)),
+    (8, 510, R(5, scoring="sigmoid", n_group=3, topk_group=2, group_score="top2")),
+]
+
+
+@pytest.mark.parametrize("M,E,router", CASES)
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_matches_oracle(M, E, router, with_bias, dtype):
+    g = torch.Generator().manual_seed(E)
+    bias = torch.randn(E, generator=g) * 0.1 if with_bias else None
+    _check(_logits(M, E, M * 1000 + E, dtype), router, bias)
+
+
+def test_many_tokens_with_grouped_scores():
+    r = R(8, scoring="sigmoid", n_group=8, topk_group=4, group_score="top2", renormalize=True, scale=2.5)
+    g = torch.Generator().manual_seed(3)
+    _check(_logits(3001, 256, 11), r, torch.randn(256, generator=g) * 0.1)
+
+
+@pytest.mark.parametrize("router", [R(4), R(4, renormalize=True), R(4, scoring="sigmoid", renormalize=True),
+                                    R(4, n_group=4, topk_group=2), R(4, n_group=4, topk_group=2, group_score="top2")])
+def test_masked_logits(router):
+    """-inf, NaN, +inf and the type's lowest value; rows with nothing, one and few live experts."""
+    inf, nan, low = math.inf, math.nan, torch.finfo(torch.float32).min
+    l = _logits(10, 16, 5)
+    l[0] = -inf
+    l[1] = nan
+    l[2] = -inf
+    l[2, 9] = 0.5
+    l[3, ::2] = nan
+    l[4, 5:] = -inf
+    l[5] = low
+    l[6, :] = -inf
+    l[6, [1, 14]] = torch.tensor([low, 3.0])
+    l[7, 3] = inf
+    l[7, 12] = inf
+    l[8] = 0.0
+    l[9, :8] = -inf
+    _check(l, router)
+
+
+def test_masking_through_the_bias():
+    """A bias of -inf (or NaN) takes its expert out, +inf puts it first."""
+    l = _logits(6, 12, 8)
+    bias = torch.zeros(12)
+    bias[[2, 7]] = -math.inf
+    bias[5] = math.inf
+    _check(l, R(11, scoring="sigmoid", renormalize=True), bias)
+    _check(l, R(3), bias)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_ties_go_to_the_lowest_index(scoring, group_score):
+    g = torch.Generator().manual_seed(2)
+    l = torch.randint(-2, 3, (64, 96), generator=g).float()
+    for r in (R(6, scoring=scoring), R(6, scoring=scoring, n_group=8, topk_group=3, group_score=group_score)):
+        _check(l, r)
+        _check(l, r, torch.full((96,), 0.25))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_picks_closer_than_fp32_scores(scoring):
+    """Biases that make all scores + bias nearly equal: only the fp32 rounding of the bias (2^-25
+    relative, far below what an fp32 score resolves) tells them apart, and it has to."""
+    for seed in range(4):
+        l = _logits(1, 64, 40 + seed)
+        p = torch.softmax(l.double(), 1) if scoring == "softmax" else torch.sigmoid(l.double())
+        bias = (0.7 - p[0]).float()
+        _check(l.expand(8, 64).contiguous(), R(8, scoring=scoring), bias)
+        _check(l, R(8, scoring=scoring, n_group=8, topk_group=3, group_score="top2"), bias)
+
+
+def test_extreme_logits():
+    l = torch.tensor([[1e30, -1e30, 3e38, -3e38, 0.0, 88.0, -104.0, 1e-40]])
+    for r in (R(8), R(8, scoring="sigmoid"), R(4, renormalize=True), R(8, scoring="sigmoid", renormalize=True)):
+        _check(l, r)
+    # sigmoid scores that underflow in fp32 keep their ratio when renormalised
+    _check(torch.tensor([[-200.0, -201.0, -230.0, -199.5]]), R(3, scoring="sigmoid", renormalize=True))
+
+
+def test_strides_views_and_empty():
+    wide = _logits(9, 200, 3).to(gpu())
+    view = wide[1:, 7:107]  # odd element offset, row stride 200
+    ids, w = ops.moe_route(view, R(4))
+    i2, w2 = ops.moe_route(view.contiguous(), R(4))
+    assert torch.equal(ids, i2) and torch.equal(w, w2)
+    t = ops.moe_route(wide.t()[:64], R(2))
+    t2 = ops.moe_route(wide.t()[:64].contiguous(), R(2))
+    assert torch.equal(t[0], t2[0]) and torch.equal(t[1], t2[1])
+    e = ops.moe_route(wide[:1].expand(4, 200), R(2))
+    assert torch.equal(e[0], ops.moe_route(wide[:1], R(2))[0].expand(4, 2))
+    ids, w = ops.moe_route(wide[:0], R(4))
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+
+
+def test_rows_behind_the_last_are_left_alone():
+    from mxfp4_block_scaled_expert_amd import _lib as L
+    l = _logits(5, 40, 9).to(gpu())
+    ids = torch.full((8, 3), -7, dtype=torch.int32, device=gpu())
+    w = torch.full((8, 3), -7.0, device=gpu())
+    st = L.load().mxq_moe_route(l.data_ptr(), L.MXQ_DTYPE_F32, 5, 40, 40, ops._router(R(3)), None, ids.data_ptr(),
+                                w.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (ids[5:] == -7).all() and (w[5:] == -7).all() and (ids[:5] >= 0).all()
