@@ -564,9 +564,9 @@ mxq_status mxq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, in
  *   out        bf16 [M, H], row stride ldo elements (ldo >= H); a token without a live expert gets zeros
  *   workspace  mxq_moe_layer_workspace_size(M, H, I, E, topk, weights) bytes (0: sizes the layer does
  *              not take), contents arbitrary; concurrent calls need workspaces of their own
- *   H and I multiples of 128 (FP8) or 32 (MXFP4); E <= 512; the rows of one token have to fit the
- *   GPU's on-chip memory (H up to about 70000, I up to about 18000), else MXQ_ERR_SHAPE.  Experts
- *   that no token chose are never read. */
+ *   H and I multiples of 128 (FP8) or 32 (MXFP4); E <= 512; one token's row of x has to fit a
+ *   compute unit's LDS (H up to about 60000), one expert's weights 2 GiB, I <= 2^20 and
+ *   M * topk * I < 2^29, else MXQ_ERR_SHAPE.  Experts that no token chose are never read. */
 size_t mxq_moe_layer_workspace_size(int64_t M, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t weights);
 mxq_status mxq_moe_layer_fp8(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, int64_t ldx, const void* gate,
                              int32_t gate_dtype, const float* gate_bias, const mxq_moe_router* router,

@@ -912,7 +912,7 @@ mxq_status read_router(const mxq_moe_router* r, int32_t E, const float* correcti
 
 // Regions of the few-token layer's workspace.
 struct LayerWs {
-  size_t part, h, total;
+  size_t part, rows, h, total;
   int32_t S, chunk, pass;
 };
 
@@ -922,17 +922,18 @@ bool layer_ws(int64_t M, int64_t H, int64_t I, int32_t E, int32_t topk, int32_t 
   if (weights != MXQ_WEIGHTS_FP8_BLOCK && weights != MXQ_WEIGHTS_MXFP4) return false;
   if (M < 1 || M > kLayerMaxTokens || H < unit || I < unit || H % unit != 0 || I % unit != 0) return false;
   if (E < 1 || E > kRouteMaxExperts || topk < 1 || topk > kRouteMaxTopk || topk > E) return false;
-  // one expert's weights are addressed with 32-bit byte offsets (rows padded to 256 elements)
-  constexpr int64_t k4G = int64_t(1) << 32;
-  if (H > (1 << 20) || I > (1 << 20) || 2 * I * (H + 256) >= k4G || H * (I + 256) >= k4G) return false;
+  // one expert's weights (rows padded to 256 elements) and the pass's intermediate lie below 2 GiB
+  constexpr int64_t k2G = int64_t(1) << 31;
+  if (H > (1 << 20) || I > (1 << 20) || 2 * I * (H + 256) >= k2G || H * (I + 256) >= k2G) return false;
   const int wfmt = weights == MXQ_WEIGHTS_MXFP4 ? W_E2M1_MX : W_E4M3_BLOCK;
   w.pass = layer_pass_tokens(wfmt, H, E, topk);
   if (w.pass < 1) return false;
   w.pass = int32_t(std::min<int64_t>(w.pass, M));
-  if (layer_batch_rows(wfmt, I, E, w.pass * topk) < 1) return false;
+  if (int64_t(w.pass) * topk * I >= (int64_t(1) << 29)) return false;  // h within 32-bit byte offsets
   layer_gate_split(E, H, w.S, w.chunk);
   w.part = 0;
-  w.h = align256(size_t(w.S) * size_t(M) * size_t(E) * 4);
+  w.rows = align256(size_t(w.S) * size_t(M) * size_t(E) * 4);
+  w.h = w.rows + align256(size_t(1 + 2 * w.pass * topk + E) * 4);
   w.total = w.h + align256(size_t(w.pass) * size_t(topk) * 2 * size_t(I) * 2);
   return true;
 }
@@ -974,6 +975,7 @@ mxq_status run_layer(const void* x, int64_t M, int64_t H, int64_t I, int32_t E, 
   a.part = reinterpret_cast<float*>(base + ws.part);
   a.S = ws.S;
   a.chunk = ws.chunk;
+  a.rows = reinterpret_cast<int32_t*>(base + ws.rows);
   a.h = reinterpret_cast<uint16_t*>(base + ws.h);
   a.out = static_cast<uint16_t*>(out);
   a.ldo = ldo;

@@ -297,15 +297,16 @@ struct LayerArgs {
   float* part;              // [S][M_all][E] partial logits
   int32_t S, chunk;         // K chunks of the router product
   uint16_t* h;              // [sorted row][hi, lo][I] bf16
-  int32_t B;                // sorted rows per batch of the down stage
+  int32_t* rows;            // the pass's routing for the down stage, R = M * topk: row count | [R] sorted
+                            // rows (expert << 8 | token) | [R] sorted row of flat row t * topk + k or -1
+                            // | [E] tokens of each expert, one bit per token
   uint16_t* out;            // bf16 [M_all, H], row stride ldo elements
   int64_t ldo;
 };
-// Tokens one pass of the expert stages can take (their rows of x lie in LDS), the K chunks of the
-// router product, and the down stage's batch.
+// Tokens one pass of the expert stages can take (their rows of x lie in LDS), and the K chunks of
+// the router product.
 int layer_pass_tokens(int wfmt, int64_t H, int32_t E, int32_t topk);
 void layer_gate_split(int32_t E, int64_t H, int32_t& S, int32_t& chunk);
-int layer_batch_rows(int wfmt, int64_t I, int32_t E, int32_t rows);
 void launch_moe_layer(const LayerArgs& a, hipStream_t stream);
 
 // Linear with 4-bit weights and group scales (int4.hip).

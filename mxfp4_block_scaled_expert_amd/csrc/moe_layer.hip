@@ -18,12 +18,15 @@
 //    go to the workspace and are added in order where they are read.
 //  * moe_up_kernel: every workgroup routes all tokens itself (one wave per token: the logits are
 //    a few KB) and builds the same tables in LDS: chosen experts ascending, each with its rows
-//    (tokens ascending).  A wave's item is 16 gate columns and the 16 matching up columns of one
-//    expert over the whole K, so its epilogue has both halves in registers.
+//    (tokens ascending).  An item is 16 gate columns and the 16 matching up columns of one expert;
+//    a wave takes it over the whole K, or, where items are fewer than half the waves, two, four or
+//    eight waves share its K steps and meet in LDS.
 //  * moe_down_kernel: a workgroup's item is 16 output columns over ALL chosen experts; its eight
-//    waves split the (expert rows, K steps) evenly, and their sums meet in LDS, each token's rows
-//    added in a fixed order -- no partial outputs in memory, no atomics, no combine launch.  The
-//    rows of h are copied into LDS in batches of B sorted rows, one batch ahead.
+//    waves split the (segments of at most kDownRows rows of an expert) x (K steps) evenly, each
+//    fetching the h rows of its own steps through registers into a few KB of LDS of its own, and
+//    their sums meet in LDS once an item, each token's rows added in a fixed order -- no partial
+//    outputs in memory, no atomics, no combine launch.  (A first version staged the h rows for the
+//    whole workgroup, a barrier per four rows: 110 us against 60 us for 16 MXFP4 tokens.)
 //
 // Rounding: products and sums are fp32.  The routing weight joins h in fp32.  h is kept as two
 // bf16 terms (hi + lo, relative error 2^-17 of it): with one bf16 term the output's error against
@@ -31,7 +34,6 @@
 // hi and lo are simply two rows of the same product.
 #include <algorithm>
 
-#include "lds_dma.hpp"
 #include "kernels.hpp"
 #include "route_common.hpp"
 
@@ -40,8 +42,20 @@ namespace mxq {
 namespace {
 constexpr int kLyThreads = 512, kLyWaves = 8;
 constexpr int kGateThreads = 256;
-constexpr int kUpD = 4;    // ring depth of the gate/up stream: 3 steps of 4 KB per wave in flight
-constexpr int kDownD = 8;  // of the down stream: 7 steps of 2 KB
+constexpr int kDownRows = 4;  // rows of an expert that one pass over its weights takes in the down stage
+// Steps in the weight rings (that many less one on their way while one is multiplied).  Deeper rings
+// were measured slower for one token and no faster for many: depths 3 / 4, 4 / 6, 8 / 6 of gate-up /
+// down took 35, 36, 41 us (one MXFP4 token) and 147, 147, 152 us (16 tokens).
+constexpr int kUpD = 3, kDownD = 4;
+constexpr int kDownRows = 4;  // rows of an expert that one pass over its weights takes in the down stage
+#ifndef UPD
+#define UPD 3
+#endif
+#ifndef DND
+#define DND 4
+#endif
+constexpr int kUpD = UPD;    // ring depth of the gate/up stream: 3 steps of 4 KB per wave in flight
+constexpr int kDownD = DND;  // of the down stream: 7 steps of 2 KB
 }  // namespace
 
 // ---------------------------------------------------------------- router product
@@ -95,7 +109,8 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_kernel(const uint16_t* 
 
 // ---------------------------------------------------------------- routing tables in LDS
 
-struct LayerTables {
+// What the gate/up stage needs to know about the routing.
+struct UpTables {
   int32_t* mask;    // [E] tokens of each expert, one bit per token
   int32_t* start;   // [E] first sorted row of each expert
   int32_t* touch;   // [E] chosen experts, ascending
@@ -103,17 +118,13 @@ struct LayerTables {
   float* w;         // [R]
   int32_t* row;     // [R] sorted rows: expert << 8 | token
   float* roww;      // [R] their routing weights
-  int32_t* seg;     // [R] segments: runs of one expert inside a batch of B rows: expert << 16 | first row
-  int32_t* misc;    // rows, chosen experts, segments, (spare)
-  int32_t* bseg;    // [R + 1] first segment of each batch
+  int32_t* misc;    // rows, chosen experts
 };
 
-__host__ __device__ inline uint32_t layer_table_bytes(int E, int R) {
-  return uint32_t((4 * (3 * E + 5 * R + 4 + R + 1) + 15) & ~15);
-}
+__host__ __device__ inline uint32_t up_table_bytes(int E, int R) { return uint32_t((4 * (3 * E + 4 * R + 2) + 15) & ~15); }
 
-__device__ __forceinline__ LayerTables layer_tables(uint8_t* p, int E, int R) {
-  LayerTables t;
+__device__ __forceinline__ UpTables up_tables(uint8_t* p, int E, int R) {
+  UpTables t;
   int32_t* q = reinterpret_cast<int32_t*>(p);
   t.mask = q; q += E;
   t.start = q; q += E;
@@ -122,15 +133,14 @@ __device__ __forceinline__ LayerTables layer_tables(uint8_t* p, int E, int R) {
   t.w = reinterpret_cast<float*>(q); q += R;
   t.row = q; q += R;
   t.roww = reinterpret_cast<float*>(q); q += R;
-  t.seg = q; q += R;
-  t.misc = q; q += 4;
-  t.bseg = q;
+  t.misc = q;
   return t;
 }
 
-// Every thread of the workgroup calls it; `scratch`: E floats per wave.
+// Routes the pass's tokens and groups their rows by expert.  Every thread of the workgroup calls
+// it; `scratch`: E floats per wave where the router has groups.
 template <int KPL>
-__device__ __forceinline__ void build_tables(const LayerArgs& a, const LayerTables& T, float* scratch, int B) {
+__device__ __forceinline__ void build_tables(const LayerArgs& a, const UpTables& T, float* scratch) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = a.rt.E, topk = a.rt.topk, M = a.M, R = M * topk;
   for (int e = tid; e < E; e += kLyThreads) T.mask[e] = 0;
@@ -143,12 +153,24 @@ __device__ __forceinline__ void build_tables(const LayerArgs& a, const LayerTabl
       l[i] = -__builtin_huge_valf();
       b[i] = 0.f;
       if (e < E) {
-        float s = a.gate_bias ? a.gate_bias[e] : 0.f;
-        const float* p = a.part + int64_t(t + a.t0) * E + e;
-        for (int c = 0; c < a.S; ++c) s += p[int64_t(c) * a.M_all * E];
-        l[i] = s;
+        l[i] = a.gate_bias ? a.gate_bias[e] : 0.f;
         if (a.rt.bias) b[i] = a.rt.bias[e];
       }
+    }
+    // the K chunks' sums in chunk order, four chunks' reads on their way together
+    const float* p = a.part + int64_t(t + a.t0) * E + lane * KPL;
+    const int64_t slice = int64_t(a.M_all) * E;
+    for (int c0 = 0; c0 < a.S; c0 += 4) {
+      float v[4][KPL];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < KPL; ++i)
+          v[c][i] = lane * KPL + i < E && c0 + c < a.S ? p[(c0 + c) * slice + i] : 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) l[i] += v[c][i];
     }
     bool close;
     const RouteSlot s = route_token<KPL, float>(l, b, a.rt, scratch + wave * E, close);
@@ -193,52 +215,51 @@ __device__ __forceinline__ void build_tables(const LayerArgs& a, const LayerTabl
   __syncthreads();
   for (int r = tid; r < R; r += kLyThreads) {
     const int e = T.id[r], t = r / topk;
-    if (e < 0) continue;
-    const int j = T.start[e] + __popc(T.mask[e] & ((1 << t) - 1));
+    const int j = e < 0 ? -1 : T.start[e] + __popc(T.mask[e] & ((1 << t) - 1));
+    if (blockIdx.x == 0) a.rows[1 + R + r] = j;  // for the down stage
+    if (j < 0) continue;
     T.row[j] = e << 8 | t;
     T.roww[j] = T.w[r];
   }
   __syncthreads();
-  if (B > 0 && wave == 0) {
-    const int rows = T.misc[0];
-    int n = 0;
-    for (int j0 = 0; j0 < rows; j0 += 64) {
-      const int j = j0 + lane;
-      const bool first = j < rows && (j % B == 0 || (T.row[j] >> 8) != (T.row[j - 1] >> 8));
-      const uint64_t m = __ballot(first);
-      const int at = n + __popcll(m & ((uint64_t(1) << lane) - 1));
-      if (first) {
-        T.seg[at] = (T.row[j] >> 8) << 16 | j;
-        if (j % B == 0) T.bseg[j / B] = at;
-      }
-      n += __popcll(m);
-    }
-    if (lane == 0) {
-      T.misc[2] = n;
-      T.bseg[(rows + B - 1) / B] = n;
-    }
-  }
-  __syncthreads();
+}
+
+// The down stage's: the sorted rows, and their segments -- at most kDownRows rows of one expert.
+struct DownTables {
+  int32_t* pos;     // [R] sorted row of flat row t * topk + k, -1: none
+  int32_t* segof;   // [R] segment of each sorted row
+  int32_t* seg;     // [R] expert << 16 | first row
+  int32_t* misc;    // segments
+};
+
+__host__ __device__ inline uint32_t down_table_bytes(int R) { return uint32_t((4 * (3 * R + 1) + 15) & ~15); }
+
+__device__ __forceinline__ DownTables down_tables(uint8_t* p, int R) {
+  int32_t* q = reinterpret_cast<int32_t*>(p);
+  return DownTables{q, q + R, q + 2 * R, q + 3 * R};
 }
 
 // ---------------------------------------------------------------- weight streams
 
 // One 128-byte step of a lane's weight rows in the ring: G 16-row groups, lane (l16, q) holds bytes
-// [32 q, +32) of row l16's step (the same bytes from both layouts), with what scales them: MXFP4
-// the two e8m0 codes of those bytes' 32-element groups; FP8 the 128 x 128 block's scale.
+// [64 h + 16 q, +16), h = 0, 1, of row l16's step, so one read of a wave takes whole 64-byte pieces
+// of the plain layout's rows (256-byte pieces of the tiled layout) -- with half-filled pieces
+// (32 q + 16 h) the plain layout's layer of one MXFP4 token took 63 us against 36 us tiled.  With
+// them what scales them: MXFP4 the e8m0 codes of those bytes' 32-element groups; FP8 the 128 x 128
+// block's scale.
 template <int WFMT, int G>
 struct WStep {
   i32x4 w[G][2];
   uint32_t s[G][WFMT == W_E2M1_MX ? 2 : 1];
 };
 
-// Where a 16-row group's bytes come from.
+// Where 16-row groups' bytes come from: one expert's weights and scales as buffers, this lane's
+// byte offsets in them.
 template <int G>
 struct WGeo {
-  const uint8_t* w;   // expert base (uniform)
-  const uint8_t* s;
-  uint32_t woff[G];   // plain: row * row_bytes;  tiled: first tile of the group + 16 lane
-  uint32_t soff[G];   // MXFP4 plain: row * groups, tiled: first tile + 2 lane;  FP8: byte offset of the block row
+  __amdgpu_buffer_rsrc_t w, s;
+  uint32_t woff[G];   // plain: row * row bytes + 16 q;  tiled: the lane's first byte in the group's first tile
+  uint32_t soff[G];   // MXFP4 plain: row * groups + q, tiled: likewise;  FP8: the block row
 };
 
 // Matrix of one stage: [E][N rows][K].
@@ -267,86 +288,142 @@ __device__ __forceinline__ WMat wmat(const uint8_t* w, const uint8_t* s, int N, 
   return m;
 }
 
-// Geometry of group g of expert e: rows [16 grp, +16).
+constexpr uint32_t kNoRead = 0x80000000u;  // a byte offset past every buffer's end (the host keeps them below)
+constexpr int kRaw = 0x00027000;           // a raw buffer resource's last word
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t raw_buffer(const uint8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, int(bytes), kRaw);
+}
+
+// Expert e's buffers.  Reads past a buffer's end return zeros and touch no memory.
+template <int G>
+__device__ __forceinline__ void geo_expert(WGeo<G>& o, const WMat& m, int e) {
+  o.w = raw_buffer(m.w + int64_t(e) * m.w_estride, uint32_t(m.w_estride));
+  o.s = raw_buffer(m.s + int64_t(e) * m.s_estride, uint32_t(m.s_estride));
+}
+
+// One of two geometries by a uniform choice.
+template <int G>
+__device__ __forceinline__ WGeo<G> geo_pick(bool second, const WGeo<G>& a, const WGeo<G>& b) {
+  WGeo<G> o;
+  o.w = second ? b.w : a.w;
+  o.s = second ? b.s : a.s;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    o.woff[g] = second ? b.woff[g] : a.woff[g];
+    o.soff[g] = second ? b.soff[g] : a.soff[g];
+  }
+  return o;
+}
+
+// Group g is the 16 rows [16 grp, +16).
 template <int WFMT, bool TILED, int G>
 __device__ __forceinline__ void geo_group(WGeo<G>& o, const WMat& m, int g, int grp) {
   constexpr bool MX = WFMT == W_E2M1_MX;
-  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   if (TILED) {
-    o.woff[g] = uint32_t(grp) * uint32_t(m.nsteps) * 2048u + uint32_t(lane) * 16u;
-    if (MX) o.soff[g] = uint32_t(grp) * uint32_t(m.nsteps) * 128u + uint32_t(lane) * 2u;
+    // bytes 64 h + 16 q of a row's step are chunk (q & 1) of lane group 2 h + q / 2 in the tile
+    o.woff[g] = uint32_t(grp) * uint32_t(m.nsteps) * 2048u + uint32_t((q & 1) * 1024 + (q >> 1) * 256 + l16 * 16);
+    if (MX) o.soff[g] = uint32_t(grp) * uint32_t(m.nsteps) * 128u + uint32_t((q & 1) + (q >> 1) * 32 + l16 * 2);
   } else {
     const uint32_t row = uint32_t(grp) * 16u + uint32_t(l16);
-    o.woff[g] = row * uint32_t(MX ? m.K / 2 : m.K);
-    if (MX) o.soff[g] = row * uint32_t(m.K / 32);
+    o.woff[g] = row * uint32_t(MX ? m.K / 2 : m.K) + uint32_t(q) * 16u;
+    if (MX) o.soff[g] = row * uint32_t(m.K / 32) + uint32_t(q);
   }
   if (!MX) o.soff[g] = uint32_t(grp >> 3) * uint32_t(m.K / 128) * 4u;
 }
 
-// `vzero`: a zero the compiler does not know to be one, in a vector register, so that the FP8 block
-// scales come through the vector memory path like the weights (a scalar load would share its
-// counter with the LDS reads, which would then wait for it).
+// Step st (uniform) of the groups: the lane offsets stay as they are along a row, the step goes into
+// the scalar offset.  Nothing is read past st_end, nor of chunks past a row's end (MXFP4 rows that
+// end inside a step).
 template <int WFMT, bool TILED, int G>
-__device__ __forceinline__ void wload(WStep<WFMT, G>& o, const WGeo<G>& gm, const WMat& m, int st, uint32_t vzero) {
+__device__ __forceinline__ void wload(WStep<WFMT, G>& o, const WGeo<G>& gm, const WMat& m, int st, int st_end) {
   constexpr bool MX = WFMT == W_E2M1_MX;
-  const int lane = threadIdx.x & 63, q = lane >> 4;
-  const uint32_t sc = uint32_t(st);
-  if constexpr (TILED) {
-    // a row that ends inside its last step is zero-padded there; its padding chunks re-read the
-    // row's first chunk of that step (a line lanes 0-15 fetch anyway)
-    uint32_t h0 = 0u, h1 = 1024u;
-    if (MX && st == m.nsteps - 1) {
-      const uint32_t rest = uint32_t(m.K / 2 - (m.nsteps - 1) * 128);
-      if (32u * uint32_t(q) + 16u > rest) h0 = 0u - 256u * uint32_t(q);
-      if (32u * uint32_t(q) + 32u > rest) h1 = 0u - 256u * uint32_t(q);
-    }
+  // the tiled layout's pieces are read once and whole: non-temporal (6.6 against 5.9 TB/s streaming);
+  // the plain layout's 64-byte pieces want the line's other half to stay (5.1 against 5.7 TB/s)
+  constexpr int kNt = TILED ? 2 : 0;
+  const int q = (threadIdx.x & 63) >> 4;
+  const int wo = st * (TILED ? 2048 : 128), so = MX ? st * (TILED ? 128 : 8) : st * 4;
+  const bool dead = st >= st_end;
+  bool no0 = dead, no1 = dead;
+  if (MX) {
+    const int rest = m.K / 2 - (m.nsteps - 1) * 128 - q * 16;  // bytes of the last step from this lane's first
+    const bool last = st == m.nsteps - 1;
+    no0 = dead || (last && rest <= 0);
+    no1 = dead || (last && rest <= 64);
+  }
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      o.w[g][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(gm.w + (gm.woff[g] + sc * 2048u + h0)));
-      o.w[g][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(gm.w + (gm.woff[g] + sc * 2048u + h1)));
-      if (MX) {
-        const uint32_t v = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(gm.s + gm.soff[g] + sc * 128u));
-        o.s[g][0] = v;
-      }
-    }
-  } else {
-    const uint32_t row_bytes = uint32_t(MX ? m.K / 2 : m.K);
-    uint32_t b0 = sc * 128u + uint32_t(q) * 32u, b1 = b0 + 16u;
-    const uint32_t ngroups = uint32_t(m.K / 32);
-    const uint32_t g0 = min(sc * 8u + 2u * uint32_t(q), ngroups - 1), g1 = min(sc * 8u + 2u * uint32_t(q) + 1u, ngroups - 1);
-    // 16-byte chunks past the row's end re-read its first one: finite codes times zero padding
-    if (MX && b0 >= row_bytes) b0 = 0;
-    if (MX && b1 >= row_bytes) b1 = 0;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      o.w[g][0] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(gm.w + (gm.woff[g] + b0)));
-      o.w[g][1] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(gm.w + (gm.woff[g] + b1)));
-      if constexpr (MX) {
-        o.s[g][0] = gm.s[gm.soff[g] + g0];
-        o.s[g][1] = gm.s[gm.soff[g] + g1];
-      }
+  for (int g = 0; g < G; ++g) {
+    const uint32_t w0 = no0 ? kNoRead : gm.woff[g], w1 = no1 ? kNoRead : gm.woff[g] + (TILED ? 512u : 64u);
+    o.w[g][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(gm.w, w0, wo, kNt));
+    o.w[g][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(gm.w, w1, wo, kNt));
+    if constexpr (MX) {
+      const uint32_t s0 = no0 ? kNoRead : gm.soff[g], s1 = no1 ? kNoRead : gm.soff[g] + (TILED ? 64u : 4u);
+      o.s[g][0] = __builtin_amdgcn_raw_buffer_load_b8(gm.s, s0, so, 0);
+      o.s[g][1] = __builtin_amdgcn_raw_buffer_load_b8(gm.s, s1, so, 0);
+    } else {
+      o.s[g][0] = __builtin_amdgcn_raw_buffer_load_b32(gm.s, dead ? kNoRead : gm.soff[g], so, 0);
     }
   }
-  if constexpr (!MX) {
+}
+
+// acc += step of rows held in LDS with chunk c of row r in slot c ^ r, one group.  at[i]: this lane's
+// chunk i (of four, MXFP4; two, FP8) in the first half of its row's step; the second half follows
+// HALF bytes on.
+template <int WFMT>
+struct RowAt {
+  static constexpr int N = WFMT == W_E2M1_MX ? 4 : 2, HALF = WFMT == W_E2M1_MX ? 256 : 128;
+  const uint8_t* p[N];
+};
+template <int WFMT>
+__device__ __forceinline__ RowAt<WFMT> row_at(const uint8_t* base, int r) {
+  constexpr int N = RowAt<WFMT>::N;
+  const int q = (threadIdx.x & 63) >> 4;
+  RowAt<WFMT> o;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-      o.s[g][0] = *reinterpret_cast<const uint32_t*>(gm.s + (gm.soff[g] + sc * 4u + vzero));
+  for (int i = 0; i < N; ++i) o.p[i] = base + r * (2 * RowAt<WFMT>::HALF) + (((q * N + i) ^ r) * 16);
+  return o;
+}
+
+template <int WFMT>
+__device__ __forceinline__ void wcompute_rows(f32x4& acc, const WStep<WFMT, 1>& v, const RowAt<WFMT>& at) {
+  if constexpr (WFMT == W_E2M1_MX) {
+    const float e0 = e8m0_to_f32(v.s[0][0]), e1 = e8m0_to_f32(v.s[0][1]);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const i32x4 af = *reinterpret_cast<const i32x4*>(at.p[s & 3] + (s >> 2) * RowAt<WFMT>::HALF);
+      uint32_t o[4];
+      e2m1x8_to_bf16(uint32_t(v.w[0][s >> 2][s & 3]), s < 4 ? e0 : e1, o);
+      acc = mfma_16x16x32_bf16(af, i32x4{int(o[0]), int(o[1]), int(o[2]), int(o[3])}, acc);
+    }
+  } else {
+    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const i32x4 af = *reinterpret_cast<const i32x4*>(at.p[s & 1] + (s >> 1) * RowAt<WFMT>::HALF);
+      uint32_t o0, o1, o2, o3;
+      e4m3x4_to_bf16(uint32_t(v.w[0][s >> 1][(2 * s) & 3]), o0, o1);
+      e4m3x4_to_bf16(uint32_t(v.w[0][s >> 1][(2 * s + 1) & 3]), o2, o3);
+      part = mfma_16x16x32_bf16(af, i32x4{int(o0), int(o1), int(o2), int(o3)}, part);
+    }
+    const float s = __uint_as_float(v.s[0][0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = fmaf(part[k], s, acc[k]);
   }
 }
 
 // acc[g] += A-step x weight-step.  arow: this lane's LDS row (its 16-byte-aligned start).
-template <int WFMT, bool TILED, int G>
+template <int WFMT, int G>
 __device__ __forceinline__ void wcompute(f32x4 (&acc)[G], const WStep<WFMT, G>& v, const uint8_t* arow, int st) {
   const int lane = threadIdx.x & 63, q = lane >> 4;
   if constexpr (WFMT == W_E2M1_MX) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      const i32x4 af = *reinterpret_cast<const i32x4*>(arow + (st * 256 + q * 64 + 8 * s) * 2);
+      const i32x4 af = *reinterpret_cast<const i32x4*>(arow + (st * 256 + (s >> 2) * 128 + q * 32 + (s & 3) * 8) * 2);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint32_t o[4];
-        const uint32_t e = TILED ? (v.s[g][0] >> (8 * (s >> 2))) & 0xffu : v.s[g][s >> 2];
-        e2m1x8_to_bf16(uint32_t(v.w[g][s >> 2][s & 3]), e8m0_to_f32(e), o);
+        e2m1x8_to_bf16(uint32_t(v.w[g][s >> 2][s & 3]), e8m0_to_f32(v.s[g][s >> 2]), o);
         acc[g] = mfma_16x16x32_bf16(af, i32x4{int(o[0]), int(o[1]), int(o[2]), int(o[3])}, acc[g]);
       }
     }
@@ -356,7 +433,7 @@ __device__ __forceinline__ void wcompute(f32x4 (&acc)[G], const WStep<WFMT, G>& 
     for (int g = 0; g < G; ++g) part[g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const i32x4 af = *reinterpret_cast<const i32x4*>(arow + (st * 128 + q * 32 + 8 * s) * 2);
+      const i32x4 af = *reinterpret_cast<const i32x4*>(arow + (st * 128 + (s >> 1) * 64 + q * 16 + (s & 1) * 8) * 2);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint32_t o0, o1, o2, o3;
@@ -374,15 +451,9 @@ __device__ __forceinline__ void wcompute(f32x4 (&acc)[G], const WStep<WFMT, G>& 
   }
 }
 
-__device__ __forceinline__ uint32_t opaque_zero() {
-  uint32_t z;
-  asm volatile("v_mov_b32 %0, 0" : "=v"(z));
-  return z;
-}
-
 // ---------------------------------------------------------------- gate / up
 
-// LDS: tables | x rows [M][row_stride] (the routing's group scratch lies there first)
+// LDS: tables | x rows [M][row_stride] | the routing's group scratch
 __host__ __device__ inline uint32_t layer_row_stride(bool mx, int K) {
   const int st = mx ? 256 : 128;
   return uint32_t((K + st - 1) / st * st * 2 + 16);  // +16 B: rows read together fall in different banks
@@ -396,69 +467,60 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
   const int E = a.rt.E, R = a.M * a.rt.topk, H = int(a.H), I = int(a.I);
-  const LayerTables T = layer_tables(smem, E, R);
-  uint8_t* const xs = smem + layer_table_bytes(E, R);
-  build_tables<KPL>(a, T, reinterpret_cast<float*>(xs), 0);
+  const UpTables T = up_tables(smem, E, R);
+  uint8_t* const xs = smem + up_table_bytes(E, R);
 
   // ---- the tokens' rows into LDS, zero-padded to whole steps
   const uint32_t stride = layer_row_stride(MX, H);
   const int chunks = int(stride / 16) - 1, valid = H / 8;
-  for (int c = tid; c < a.M * chunks; c += kLyThreads) {
-    const int t = c / chunks, cc = c - t * chunks;
-    i32x4 v = {0, 0, 0, 0};
-    if (cc < valid) v = *reinterpret_cast<const i32x4*>(a.x + (t + a.t0) * a.ldx + cc * 8);
-    *reinterpret_cast<i32x4*>(xs + t * stride + cc * 16) = v;
+  for (int t = 0; t < a.M; ++t)
+    for (int c = tid; c < chunks; c += kLyThreads) {
+      i32x4 v = {0, 0, 0, 0};
+      if (c < valid) v = *reinterpret_cast<const i32x4*>(a.x + (t + a.t0) * a.ldx + c * 8);
+      *reinterpret_cast<i32x4*>(xs + t * stride + c * 16) = v;
+    }
+  build_tables<KPL>(a, T, reinterpret_cast<float*>(xs + a.M * stride));
+  if (blockIdx.x == 0) {  // for the down stage
+    const int rows = T.misc[0];
+    for (int j = tid; j < rows; j += kLyThreads) a.rows[1 + j] = T.row[j];
+    for (int e = tid; e < E; e += kLyThreads) a.rows[1 + 2 * R + e] = T.mask[e];
+    if (tid == 0) a.rows[0] = rows;
   }
-  __syncthreads();
 
-  // ---- items: (chosen expert, 16 gate + 16 up columns), dealt over the workgroups first
+  // ---- items: (chosen expert, 16 gate + 16 up columns), dealt over the workgroups first.  Where
+  // there are fewer than half as many items as waves, KS waves of a workgroup share an item, each
+  // a part of its K steps: a stream of few waves does not fill the memory system.
   const WMat m = wmat<WFMT, TILED>(a.w1, a.s1, 2 * I, H);
-  const int tiles = I / 16, total = T.misc[1] * tiles;
-  const int step = int(gridDim.x) * kLyWaves;
-  int item = wave * int(gridDim.x) + int(blockIdx.x);
-  if (item >= total) return;
-  const uint32_t vz = opaque_zero();
+  const int tiles = I / 16, total = __builtin_amdgcn_readfirstlane(T.misc[1]) * tiles;
+  const int waves = int(gridDim.x) * kLyWaves;
+  int KS = 1;
+  while (KS < kLyWaves && 2 * KS * total <= waves && 4 * KS <= m.nsteps) KS *= 2;
+  const int step = waves / KS;
+  const int sub = wave & (KS - 1);
+  const int st_lo = m.nsteps * sub / KS, st_hi = m.nsteps * (sub + 1) / KS;
+  int item = (wave / KS) * int(gridDim.x) + int(blockIdx.x);
+  if (KS == 1 && item >= total) return;
   auto geo_of = [&](int it) __attribute__((always_inline)) {
     WGeo<2> g;
     const int ti = it / tiles, nt = it - ti * tiles;
     const int e = __builtin_amdgcn_readfirstlane(T.touch[ti]);
-    g.w = m.w + int64_t(e) * m.w_estride;
-    g.s = m.s + int64_t(e) * m.s_estride;
+    geo_expert(g, m, e);
     geo_group<WFMT, TILED, 2>(g, m, 0, nt);
     geo_group<WFMT, TILED, 2>(g, m, 1, tiles + nt);
     return g;
   };
-  WStep<WFMT, 2> ring[D];
-  // load cursor: runs D - 1 steps ahead of the computation, into the next items; past the last
-  // one it stays on the last step (read again, never computed)
-  int lit = item, lst = 0;
-  WGeo<2> lg = geo_of(lit);
-  auto load = [&](int slot) __attribute__((always_inline)) {
-    wload<WFMT, TILED, 2>(ring[slot], lg, m, lst, vz);
-    if (lst + 1 < m.nsteps) {
-      ++lst;
-    } else if (lit + step < total) {
-      lit += step;
-      lst = 0;
-      lg = geo_of(lit);
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < D - 1; ++u) load(u);
-
   f32x4 acc[2];
   const uint8_t* arow = xs;
-  int rows = 0, row0 = 0, st = 0, nt = 0, ex = 0;
+  int rows = 0, row0 = 0, nt = 0;
   float bg = 0.f, bu = 0.f;
   auto begin = [&]() __attribute__((always_inline)) {
     const int ti = item / tiles;
     nt = item - ti * tiles;
-    ex = __builtin_amdgcn_readfirstlane(T.touch[ti]);
+    const int ex = __builtin_amdgcn_readfirstlane(T.touch[ti]);
     rows = __builtin_amdgcn_readfirstlane(__popc(T.mask[ex]));
     row0 = __builtin_amdgcn_readfirstlane(T.start[ex]);
     arow = xs + uint32_t(T.row[row0 + min(l16, rows - 1)] & 0xff) * stride;
     acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    st = 0;
     // (read here, behind the ring's requests so far: in finish() the wait for it would drain the ring)
     if (a.b1) {
       const float* be = a.b1 + int64_t(ex) * 2 * I + nt * 16 + l16;
@@ -482,250 +544,258 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
       o[I] = lo;
     }
   };
-  begin();
-  for (bool more = true; more;) {
+  if (item < total) {
+    // The ring: a pass over an item is padded to whole turns, so step i of every item sits in slot
+    // i % D, and the last turn requests the next item's first steps (padding requests read nothing).
+    // The code of an item's begin and end stands once: with a transition in every slot, a kernel
+    // whose waves see a few steps each spent most of its time fetching instructions.
+    const int n = st_hi - st_lo, npad = (n + D - 1) / D * D;
+    WStep<WFMT, 2> ring[D];
+    WGeo<2> cur = geo_of(item);
 #pragma unroll
-    for (int u = 0; u < D; ++u) {
-      load((u + D - 1) % D);
-      if (more) {
-        wcompute<WFMT, TILED, 2>(acc, ring[u], arow, st);
-        if (++st == m.nsteps) {
-          finish();
-          item += step;
-          more = item < total;
-          if (more) begin();
+    for (int u = 0; u < D - 1; ++u) wload<WFMT, TILED, 2>(ring[u], cur, m, st_lo + u, st_hi);
+    for (;;) {
+      const int next = item + step;
+      const bool more = next < total;
+      const WGeo<2> nxt = geo_of(more ? next : item);
+      begin();
+      for (int s0 = 0; s0 < npad; s0 += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+          const int ls = s0 + u + D - 1;
+          const bool nx = ls >= npad;
+          wload<WFMT, TILED, 2>(ring[(u + D - 1) % D], geo_pick(nx, cur, nxt), m, st_lo + (nx ? ls - npad : ls),
+                                nx && !more ? 0 : st_hi);
+          if (s0 + u < n) wcompute<WFMT, 2>(acc, ring[u], arow, st_lo + s0 + u);
         }
       }
+      if (KS > 1) break;  // (one item per wave at most)
+      finish();
+      if (!more) break;
+      item = next;
+      cur = nxt;
+    }
+  }
+  if (KS > 1) {
+    // the shares of an item meet in LDS, added in K order by the item's first wave
+    f32x4* const sums = reinterpret_cast<f32x4*>(xs + a.M * stride);
+    __syncthreads();  // the scratch's last reader is done
+    sums[(wave * 2 + 0) * 64 + lane] = acc[0];
+    sums[(wave * 2 + 1) * 64 + lane] = acc[1];
+    __syncthreads();
+    if (sub == 0 && item < total) {
+      for (int k = 1; k < KS; ++k)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const f32x4 v = sums[((wave + k) * 2 + g) * 64 + lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[g][r] += v[r];
+        }
+      finish();
     }
   }
 }
 
+
 // ---------------------------------------------------------------- down
 
-__host__ __device__ inline uint32_t layer_down_part_bytes(int B) { return uint32_t(2 * kLyWaves * B * 16 * 4); }
+// The h rows of a step in registers on their way to LDS: the step's 256 (MXFP4) or 128 (FP8) columns of the
+// hi and lo rows of a segment's kDownRows rows, 16 bytes per lane and read.
+template <int WFMT>
+struct HStep {
+  static constexpr int N = WFMT == W_E2M1_MX ? kDownRows : kDownRows / 2;
+  i32x4 v[N];
+};
 
-// LDS: tables | partial sums [2][8 waves][B][16] fp32 | h rows [nbuf][B][hi, lo][row_stride]
-template <int WFMT, bool TILED, int KPL>
+// LDS: tables | sums [2][slots][R][16] fp32 | h rows [8 waves][2 kDownRows][step columns] bf16
+__host__ __device__ inline int down_sum_rows(int R) {
+  // segments that many waves share: fewer than eight segments of at most kDownRows rows, eight
+  // shares each; else two shares of every row
+  return R * 2 > 7 * kDownRows * 8 ? R * 2 : 7 * kDownRows * 8;
+}
+
+template <int WFMT, bool TILED>
 __global__ __launch_bounds__(kLyThreads, 2) void moe_down_kernel(LayerArgs a) {
   constexpr bool MX = WFMT == W_E2M1_MX;
-  constexpr int D = kDownD;
+  constexpr int D = kDownD, SE = MX ? 256 : 128, ROWB = SE * 2;  // columns of a step, bytes of its rows in LDS
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int E = a.rt.E, R = a.M * a.rt.topk, H = int(a.H), I = int(a.I), B = a.B;
-  const LayerTables T = layer_tables(smem, E, R);
-  float* const part = reinterpret_cast<float*>(smem + layer_table_bytes(E, R));
-  const uint32_t hs_off = layer_table_bytes(E, R) + layer_down_part_bytes(B);
-  uint8_t* const hs = smem + hs_off;
-  const uint32_t hs_addr = lds_addr(smem) + hs_off;
-  build_tables<KPL>(a, T, reinterpret_cast<float*>(hs), B);
-
-  const uint32_t stride = layer_row_stride(MX, I), buf_bytes = uint32_t(2 * B) * stride;
-  const int rows = __builtin_amdgcn_readfirstlane(T.misc[0]);
-  const int nb = (rows + B - 1) / B;  // batches per item
+  const int topk = a.rt.topk, R = a.M * topk, H = int(a.H), I = int(a.I);
+  const DownTables T = down_tables(smem, R);
+  const int sum_rows = down_sum_rows(R);
+  float* const sums = reinterpret_cast<float*>(smem + down_table_bytes(R));
+  uint8_t* const hs = smem + down_table_bytes(R) + uint32_t(sum_rows) * 2 * 64 + uint32_t(wave) * (2 * kDownRows * ROWB);
   const WMat m = wmat<WFMT, TILED>(a.w2, a.s2, H, I);
   const int items = H / 16;
-  const int my = items > int(blockIdx.x) ? (items - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
 
-  // tokens with no expert at all, or none anywhere
+  // ---- tables
+  const int rows = __builtin_amdgcn_readfirstlane(a.rows[0]);
+  for (int r = tid; r < R; r += kLyThreads) T.pos[r] = a.rows[1 + R + r];
+  if (wave == 0) {
+    int n = 0;
+    for (int r0 = 0; r0 < rows; r0 += 64) {
+      const int j = r0 + lane;
+      bool first = false;
+      int e = 0;
+      if (j < rows) {
+        // an expert's rows are cut every kDownRows: row j opens a segment when its distance from
+        // its expert's first row is a multiple of that
+        const int v = a.rows[1 + j];
+        e = v >> 8;
+        const int d = __popc(a.rows[1 + 2 * R + e] & ((1 << (v & 0xff)) - 1));
+        first = d % kDownRows == 0;
+      }
+      const uint64_t mk = __ballot(first);
+      const int at = n + __popcll(mk & ((uint64_t(2) << lane) - 1)) - 1;
+      if (j < rows) T.segof[j] = at;
+      if (first) T.seg[at] = e << 16 | j;
+      n += __popcll(mk);
+    }
+    if (lane == 0) *T.misc = n;
+  }
+  __syncthreads();
+  const int nseg = __builtin_amdgcn_readfirstlane(*T.misc);
   const int tok = tid >> 4, tc = tid & 15;
-  if (nb == 0) {
+  const int my = items > int(blockIdx.x) ? (items - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
+  if (nseg == 0) {  // no token has an expert
     for (int i = 0; i < my; ++i)
       if (tok < a.M) a.out[(tok + a.t0) * a.ldo + (int64_t(blockIdx.x) + int64_t(i) * gridDim.x) * 16 + tc] = 0;
     return;
   }
   if (my == 0) return;
 
-  // zero the rows' padding to whole steps (the copies below write [0, I) of a row), and the sums
-  {
-    const int pad = int(stride / 16) - I / 8;
-    const int nrow = 2 * B * (nb > 1 ? 2 : 1);
-    for (int c = tid; c < nrow * pad; c += kLyThreads)
-      *reinterpret_cast<i32x4*>(hs + uint32_t(c / pad) * stride + uint32_t(I / 8 + c % pad) * 16) = i32x4{0, 0, 0, 0};
-    for (int c = tid; c < 2 * kLyWaves * B * 16; c += kLyThreads) part[c] = 0.f;
-  }
+  // ---- this wave's share of every item: steps [lo, hi) of the segments' nsteps each
+  const int S = nseg * m.nsteps;
+  const bool few = S < kLyWaves;  // one step per wave
+  const int lo = few ? min(wave, S) : S * wave / kLyWaves, hi = few ? min(wave + 1, S) : S * (wave + 1) / kLyWaves;
+  auto wave_of = [&](int step) __attribute__((always_inline)) { return few ? step : (kLyWaves * (step + 1) - 1) / S; };
+  auto seg_at = [&](int sg) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(T.seg[sg]); };
+  auto seg_end = [&](int sg) __attribute__((always_inline)) {
+    return sg + 1 < nseg ? __builtin_amdgcn_readfirstlane(T.seg[sg + 1]) & 0xffff : rows;
+  };
 
-  // rows of batch b (I bf16 hi, then I lo, one after the other in memory) into LDS buffer `buf`
-  const int segs = (I * 2 + 1023) / 1024;
-  auto copy_batch = [&](int b, int buf) __attribute__((always_inline)) {
-    const int j0 = b * B, n = min(B, rows - j0) * 2;
-    for (int i = wave; i < n * segs; i += kLyWaves) {
-      const int r = i / segs, s = i - r * segs;
-      const int64_t cb = int64_t(s) * 1024 + lane * 16;
-      if (cb < I * 2)
-        lds_dma16(reinterpret_cast<const uint8_t*>(a.h) + (int64_t(j0) * 2 + r) * I * 2 + cb,
-                  hs_addr + uint32_t(buf) * buf_bytes + uint32_t(r) * stride + uint32_t(s) * 1024u);
+  const uint8_t* const hp = reinterpret_cast<const uint8_t*>(a.h);
+  const uint32_t h_bytes = uint32_t(rows) * uint32_t(I) * 4u;
+  const __amdgpu_buffer_rsrc_t hb = raw_buffer(hp, h_bytes);
+  const int kl = (lane & (SE / 8 - 1)) * 8;  // this lane's first column of a step's h rows
+  const bool hpast = (m.nsteps - 1) * SE + kl >= I;
+
+  // The share is walked in parts: steps [st, st + n) of one segment, for one item.
+  struct Part {
+    int ci, p;            // item (count), position in [lo, hi)
+    int seg, st, n;
+    int row0, sm;         // the segment's first sorted row, its rows
+  };
+  auto part_at = [&](int ci, int p) __attribute__((always_inline)) {
+    Part o;
+    o.ci = ci;
+    o.p = p;
+    o.seg = p / m.nsteps;
+    o.st = p - o.seg * m.nsteps;
+    o.n = min(m.nsteps - o.st, hi - p);
+    o.row0 = seg_at(o.seg) & 0xffff;
+    o.sm = seg_end(o.seg) - o.row0;
+    return o;
+  };
+  struct Geo {
+    WGeo<1> w;
+    uint32_t h[HStep<WFMT>::N];
+  };
+  auto geo_of = [&](const Part& o) __attribute__((always_inline)) {
+    Geo g;
+    geo_expert(g.w, m, seg_at(o.seg) >> 16);
+    geo_group<WFMT, TILED, 1>(g.w, m, 0, int(blockIdx.x) + o.ci * int(gridDim.x));
+#pragma unroll
+    for (int i = 0; i < HStep<WFMT>::N; ++i) {
+      // rows of 32 (MXFP4) or 16 (FP8) chunks: hi row, lo row (, the next row's hi and lo)
+      const int r = MX ? i : 2 * i + (lane >> 5), half = MX ? lane >> 5 : (lane >> 4) & 1;
+      g.h[i] = r < o.sm ? (uint32_t(o.row0 + r) * 2u + uint32_t(half)) * uint32_t(I) * 2u + uint32_t(kl) * 2u : kNoRead;
     }
-  };
-
-  // this wave's share of batch b: steps [lo, hi) of its segments' nsteps each
-  struct Share { int seg0, lo, hi; };
-  auto share = [&](int b) __attribute__((always_inline)) {
-    Share s;
-    s.seg0 = __builtin_amdgcn_readfirstlane(T.bseg[b]);
-    const int n = (__builtin_amdgcn_readfirstlane(T.bseg[b + 1]) - s.seg0) * m.nsteps;
-    s.lo = n * wave / kLyWaves;
-    s.hi = n * (wave + 1) / kLyWaves;
-    return s;
-  };
-  const uint32_t vz = opaque_zero();
-  const int nv = my * nb;  // (item, batch) pairs
-  auto geo_of = [&](int v, int seg) __attribute__((always_inline)) {
-    WGeo<1> g;
-    const int e = __builtin_amdgcn_readfirstlane(T.seg[seg]) >> 16;
-    g.w = m.w + int64_t(e) * m.w_estride;
-    g.s = m.s + int64_t(e) * m.s_estride;
-    geo_group<WFMT, TILED, 1>(g, m, 0, int(blockIdx.x) + (v / nb) * int(gridDim.x));
     return g;
   };
-
-  // load cursor: pair lv, its share's step lp (of lhi), as segment lseg, step lst
-  int lv = -1, lp = 0, lhi = 0, lseg = 0, lst = 0;
-  WGeo<1> lg{};
-  auto next_pair = [&]() __attribute__((always_inline)) {  // the next pair with work for this wave, if any
-    int v = lv + 1;
-    while (v < nv) {
-      const Share s = share(v % nb);
-      if (s.hi > s.lo) {
-        lv = v;
-        lp = s.lo;
-        lhi = s.hi;
-        lseg = s.seg0 + s.lo / m.nsteps;
-        lst = s.lo % m.nsteps;
-        lg = geo_of(v, lseg);
-        return;
-      }
-      ++v;
-    }
-  };
-  next_pair();
-  const bool any = lv >= 0;  // (a wave may have no work at all: it only joins the barriers)
-  if (!any) {
-    lg = geo_of(0, 0);
-  }
   WStep<WFMT, 1> ring[D];
-  int issued = 0;  // ring steps requested since the last batch copy
-  auto load = [&](int slot) __attribute__((always_inline)) {
-    wload<WFMT, TILED, 1>(ring[slot], lg, m, lst, vz);
-    ++issued;
-    if (lp + 1 < lhi) {
-      ++lp;
-      if (++lst == m.nsteps) {
-        lst = 0;
-        ++lseg;
-        lg = geo_of(lv, lseg);
-      }
-    } else {
-      next_pair();  // past the last pair: the cursor stays (its last step is read again, never computed)
-    }
+  HStep<WFMT> hring[D];
+  auto load = [&](int slot, const WGeo<1>& w, const uint32_t* h0, const uint32_t* h1, bool nx, int st, int st_end)
+      __attribute__((always_inline)) {
+    wload<WFMT, TILED, 1>(ring[slot], w, m, st, st_end);
+    const bool no = st >= st_end || (MX && st == m.nsteps - 1 && hpast);
+#pragma unroll
+    for (int i = 0; i < HStep<WFMT>::N; ++i)
+      hring[slot].v[i] = __builtin_bit_cast(
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(hb, no ? kNoRead : (nx ? h1[i] : h0[i]), st * (SE * 2), 0));
   };
 
-  __syncthreads();  // the zeroed padding, before the copies
-  copy_batch(0, 0);
-#pragma unroll
-  for (int u = 0; u < D - 1; ++u) load(u);
-
-  f32x4 acc[1];
-  const uint8_t* arow = hs;
-  float sum = 0.f;  // out[tok][tc] of the current item (threads below 256)
-  int v = 0, b = 0, cp = 0, chi = 0, cseg = 0, cst = 0, j0 = 0, sm = 0;
-
-  auto begin_seg = [&]() __attribute__((always_inline)) {
-    const int sg = __builtin_amdgcn_readfirstlane(T.seg[cseg]);
-    j0 = sg & 0xffff;
-    const int end = cseg + 1 < __builtin_amdgcn_readfirstlane(T.bseg[b + 1])
-                        ? (__builtin_amdgcn_readfirstlane(T.seg[cseg + 1]) & 0xffff) : min(rows, (b + 1) * B);
-    sm = end - j0;
-    const int i = l16 & 7;
-    arow = hs + uint32_t(nb > 1 ? (v & 1) : 0) * buf_bytes +
-           uint32_t(2 * (j0 - b * B + (i < sm ? i : 0)) + (l16 >> 3)) * stride;
-    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-  // MFMA rows i and i + 8 are the two terms of h row i
-  auto end_seg = [&]() __attribute__((always_inline)) {
-    f32x4 o;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] = acc[0][r] + __shfl_xor(acc[0][r], 32, kWave);
-    float* p = part + ((v & 1) * kLyWaves + wave) * B * 16 + (j0 - b * B) * 16 + l16;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 4 * q + r;
-      if (q < 2 && i < sm) p[i * 16] = o[r];
-    }
-  };
-  auto begin_pair = [&]() __attribute__((always_inline)) {
-    const Share s = share(b);
-    cp = s.lo;
-    chi = s.hi;
-    cseg = s.seg0 + s.lo / m.nsteps;
-    cst = s.lo % m.nsteps;
-    if (cp < chi) begin_seg();
-  };
-  // pair v is done: publish its sums, take over the next batch's rows, add up pair v's sums
-  auto end_pair = [&]() __attribute__((always_inline)) {
-    const bool last_batch = b == nb - 1;
-    if (nb > 1 && v + 1 < nv) {
-      // the copies of pair v + 1's rows were issued before `issued` ring steps, each of at least
-      // two reads
-      if (issued >= D - 1)
-        wait_vmcnt<(D - 1) * 2>();
-      else
-        wait_vmcnt<0>();
-    }
+  // the item's rows are summed: each token's in the order of its experts, a row's shares in K order.
+  // One barrier an item: the sums of the next one go to the other half.
+  auto end_item = [&](int ci) __attribute__((always_inline)) {
     __syncthreads();
-    if (nb > 1 && v + 2 < nv) {
-      copy_batch((v + 2) % nb, v & 1);
-      issued = 0;
-    }
-    if (tid < 256) {
-      const float* p = part + (v & 1) * kLyWaves * B * 16;
-      const int n = min(B, rows - b * B);
-      for (int i = 0; i < n; ++i) {
-        if ((T.row[b * B + i] & 0xff) != tok) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kLyWaves; ++w) s += p[(w * B + i) * 16 + tc];
-        sum += s;
+    if (tok < a.M) {
+      float s = 0.f;
+      for (int k = 0; k < topk; ++k) {
+        const int j = T.pos[tok * topk + k];
+        if (j < 0) continue;
+        const int s0 = T.segof[j] * m.nsteps, w0 = wave_of(s0), w1 = wave_of(s0 + m.nsteps - 1);
+        const float* p = sums + ((ci & 1) * sum_rows + j) * 16 + tc;
+        float y = 0.f;
+        for (int w = 0; w <= w1 - w0; ++w) y += p[w * rows * 16];
+        s += y;
       }
-      if (last_batch) {
-        if (tok < a.M)
-          a.out[(tok + a.t0) * a.ldo + (int64_t(blockIdx.x) + int64_t(v / nb) * gridDim.x) * 16 + tc] = f2bf(sum);
-        sum = 0.f;
-      }
+      a.out[(tok + a.t0) * a.ldo + (int64_t(blockIdx.x) + int64_t(ci) * gridDim.x) * 16 + tc] = f2bf(s);
     }
-    __syncthreads();
-    // clear this wave's sums for pair v + 2
-    for (int c = lane; c < B * 16; c += 64) part[((v & 1) * kLyWaves + wave) * B * 16 + c] = 0.f;
-    ++v;
-    b = last_batch ? 0 : b + 1;
   };
 
-  wait_vmcnt<0>();
-  __syncthreads();
-  if (nb > 1 && nv > 1) {
-    copy_batch(1 % nb, 1);
-    issued = 0;
+  if (hi <= lo) {  // a wave without a share only joins the sums
+    for (int ci = 0; ci < my; ++ci) end_item(ci);
+    return;
   }
-  begin_pair();
-  while (v < nv) {
+  Part cp = part_at(0, lo);
+  Geo cg = geo_of(cp);
 #pragma unroll
-    for (int u = 0; u < D; ++u) {
-      load((u + D - 1) % D);
-      while (v < nv && cp >= chi) {  // also pairs without work for this wave
-        end_pair();
-        if (v < nv) begin_pair();
-      }
-      if (v < nv) {
-        wcompute<WFMT, TILED, 1>(acc, ring[u], arow, cst);
-        ++cp;
-        if (++cst == m.nsteps || cp == chi) {
-          end_seg();
-          cst = 0;
-          ++cseg;
-          if (cp < chi) begin_seg();
+  for (int u = 0; u < D - 1; ++u) load(u, cg.w, cg.h, cg.h, false, cp.st + u, cp.st + cp.n);
+  for (;;) {
+    const bool item_ends = cp.p + cp.n == hi;
+    const bool more = !item_ends || cp.ci + 1 < my;
+    const Part np = more ? part_at(item_ends ? cp.ci + 1 : cp.ci, item_ends ? lo : cp.p + cp.n) : cp;
+    const Geo ng = geo_of(np);
+    const int npad = (cp.n + D - 1) / D * D, nend = more ? np.st + np.n : 0;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    // MFMA rows i and i + 8 are the hi and lo terms of the segment's row i; LDS row 2 i + term
+    const RowAt<WFMT> at = row_at<WFMT>(hs, 2 * ((l16 & 7) < cp.sm ? (l16 & 7) : 0) + (l16 >> 3));
+    for (int s0 = 0; s0 < npad; s0 += D) {
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        const int ls = s0 + u + D - 1;
+        const bool nx = ls >= npad;
+        load((u + D - 1) % D, geo_pick(nx, cg.w, ng.w), cg.h, ng.h, nx, nx ? np.st + ls - npad : cp.st + ls,
+             nx ? nend : cp.st + cp.n);
+        if (s0 + u < cp.n) {
+          // the step's h rows into this wave's LDS rows (16-byte chunk c of LDS row r in slot c ^ r)
+#pragma unroll
+          for (int i = 0; i < HStep<WFMT>::N; ++i) {
+            const int r = MX ? 2 * i + (lane >> 5) : 4 * i + (lane >> 4);
+            *reinterpret_cast<i32x4*>(hs + r * ROWB + (((lane & (SE / 8 - 1)) ^ r) * 16)) = hring[u].v[i];
+          }
+          wcompute_rows<WFMT>(acc, ring[u], at);
         }
       }
     }
+    {
+      const int slot = wave - wave_of(cp.seg * m.nsteps);
+      float* p = sums + (((cp.ci & 1) * sum_rows) + slot * rows + cp.row0) * 16 + l16;
+      f32x4 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = acc[r] + __shfl_xor(acc[r], 32, kWave);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 4 * q + r;
+        if (q < 2 && i < cp.sm) p[i * 16] = o[r];
+      }
+    }
+    if (item_ends) end_item(cp.ci);
+    if (!more) break;
+    cp = np;
+    cg = ng;
   }
 }
 
@@ -746,36 +816,34 @@ int layer_cus() {
   return cus[dev];
 }
 
-// the larger of the stage's operands and the routing's group scratch (E floats per wave)
-uint32_t with_scratch(uint32_t bytes, int E) { return std::max(bytes, uint32_t(kLyWaves * E * 4)); }
+// the shares of items (2 x 16 x 16 fp32 per wave), or before them the routing's group scratch
+// (E <= 512 floats per wave)
+constexpr uint32_t kUpScratch = kLyWaves * 2 * 256 * 4;
+static_assert(kUpScratch >= kLyWaves * kRouteMaxExperts * 4, "group scratch");
 
 uint32_t up_lds(bool mx, int64_t H, int E, int topk, int M) {
-  return layer_table_bytes(E, M * topk) + with_scratch(uint32_t(M) * layer_row_stride(mx, int(H)), E);
+  return up_table_bytes(E, M * topk) + uint32_t(M) * layer_row_stride(mx, int(H)) + kUpScratch;
 }
 
-uint32_t down_lds(bool mx, int64_t I, int E, int rows, int B) {
-  return layer_table_bytes(E, rows) + layer_down_part_bytes(B) +
-         with_scratch(uint32_t((rows > B ? 2 : 1) * 2 * B) * layer_row_stride(mx, int(I)), E);
+uint32_t down_lds(bool mx, int R) {
+  return down_table_bytes(R) + uint32_t(down_sum_rows(R)) * 2 * 64 + uint32_t(kLyWaves * 2 * kDownRows * (mx ? 512 : 256));
 }
 
-template <int WFMT, bool TILED, int KPL>
+template <int WFMT, bool TILED>
 void launch_layer_t(const LayerArgs& a, hipStream_t st) {
   constexpr bool MX = WFMT == W_E2M1_MX;
   const int R = a.M * a.rt.topk;
   const int64_t most = std::min<int64_t>(a.rt.E, R);  // chosen experts at most
   const unsigned gu = unsigned(std::min<int64_t>(layer_cus(), cdiv(most * (a.I / 16), kLyWaves)));
-  hipLaunchKernelGGL((moe_up_kernel<WFMT, TILED, KPL>), dim3(gu), dim3(kLyThreads),
-                     up_lds(MX, a.H, a.rt.E, a.rt.topk, a.M), st, a);
+  const size_t lu = up_lds(MX, a.H, a.rt.E, a.rt.topk, a.M);
+  if (a.rt.E <= 128)
+    hipLaunchKernelGGL((moe_up_kernel<WFMT, TILED, 2>), dim3(gu), dim3(kLyThreads), lu, st, a);
+  else if (a.rt.E <= 256)
+    hipLaunchKernelGGL((moe_up_kernel<WFMT, TILED, 4>), dim3(gu), dim3(kLyThreads), lu, st, a);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<WFMT, TILED, 8>), dim3(gu), dim3(kLyThreads), lu, st, a);
   const unsigned gd = unsigned(std::min<int64_t>(layer_cus(), a.H / 16));
-  hipLaunchKernelGGL((moe_down_kernel<WFMT, TILED, KPL>), dim3(gd), dim3(kLyThreads),
-                     down_lds(MX, a.I, a.rt.E, R, a.B), st, a);
-}
-
-template <int WFMT, bool TILED>
-void launch_layer_k(const LayerArgs& a, hipStream_t st) {
-  if (a.rt.E <= 128) launch_layer_t<WFMT, TILED, 2>(a, st);
-  else if (a.rt.E <= 256) launch_layer_t<WFMT, TILED, 4>(a, st);
-  else launch_layer_t<WFMT, TILED, 8>(a, st);
+  hipLaunchKernelGGL((moe_down_kernel<WFMT, TILED>), dim3(gd), dim3(kLyThreads), down_lds(MX, R), st, a);
 }
 }  // namespace
 
@@ -783,12 +851,6 @@ int layer_pass_tokens(int wfmt, int64_t H, int32_t E, int32_t topk) {
   int m = kLayerMaxTokens;
   while (m > 0 && up_lds(wfmt == W_E2M1_MX, H, E, topk, m) > kLyMaxLds) --m;
   return m;
-}
-
-int layer_batch_rows(int wfmt, int64_t I, int32_t E, int32_t rows) {
-  int B = 8;
-  while (B > 0 && down_lds(wfmt == W_E2M1_MX, I, E, rows, B) > kLyMaxLds) B /= 2;
-  return B;
 }
 
 // Enough workgroups to read the router's weights from all over the GPU, chunks of at least 512.
@@ -811,13 +873,12 @@ void launch_moe_layer(const LayerArgs& g, hipStream_t st) {
   const int pass = layer_pass_tokens(a.wfmt, a.H, a.rt.E, a.rt.topk);
   for (a.t0 = 0; a.t0 < a.M_all; a.t0 += pass) {
     a.M = std::min(pass, a.M_all - a.t0);
-    a.B = layer_batch_rows(a.wfmt, a.I, a.rt.E, a.M * a.rt.topk);
     if (a.wfmt == W_E2M1_MX) {
-      if (a.tiled) launch_layer_k<W_E2M1_MX, true>(a, st);
-      else launch_layer_k<W_E2M1_MX, false>(a, st);
+      if (a.tiled) launch_layer_t<W_E2M1_MX, true>(a, st);
+      else launch_layer_t<W_E2M1_MX, false>(a, st);
     } else {
-      if (a.tiled) launch_layer_k<W_E4M3_BLOCK, true>(a, st);
-      else launch_layer_k<W_E4M3_BLOCK, false>(a, st);
+      if (a.tiled) launch_layer_t<W_E4M3_BLOCK, true>(a, st);
+      else launch_layer_t<W_E4M3_BLOCK, false>(a, st);
     }
   }
 }

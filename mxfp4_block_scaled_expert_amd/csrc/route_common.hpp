@@ -58,6 +58,12 @@ __device__ __forceinline__ double wave_total(double v) {
   return v;
 }
 
+// Lane `src`'s value (src uniform) in every lane.
+__device__ __forceinline__ float lane_value(float v, int src) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
+}
+__device__ __forceinline__ double lane_value(double v, int src) { return __shfl(v, src, kWave); }
+
 __device__ __forceinline__ float route_exp(float x) { return expf(x); }
 __device__ __forceinline__ double route_exp(double x) { return exp(x); }
 
@@ -191,9 +197,9 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
         wl = l[i];
         wp = p[i];
       }
-    const int id = __shfl(lane * KPL + bi, win, kWave);
-    const float ll = __shfl(wl, win, kWave);
-    const T pp = __shfl(wp, win, kWave);
+    const int id = __builtin_amdgcn_readlane(lane * KPL + bi, win);
+    const float ll = lane_value(wl, win);
+    const T pp = lane_value(wp, win);
     if (lane == k) {
       out.id = id;
       my_l = ll;

@@ -65,7 +65,7 @@ def test_layer_refusals(mx):
     assert call(M=0) == L.MXQ_OK
     for bad in (dict(M=-1), dict(M=17), dict(H=240, ldx=240, ldo=240), dict(I=100), dict(H=0), dict(I=0), dict(E=0),
                 dict(E=513), dict(ldx=248), dict(ldx=260), dict(ldo=255), dict(H=1 << 21, ldx=1 << 21, ldo=1 << 21),
-                dict(H=1 << 17, ldx=1 << 17, ldo=1 << 17), dict(I=1 << 17), dict(x=C.c_void_p((1 << 20) + 8)),
+                dict(H=1 << 17, ldx=1 << 17, ldo=1 << 17), dict(I=1 << 21), dict(x=C.c_void_p((1 << 20) + 8)),
                 dict(gate=C.c_void_p((1 << 20) + 8)), dict(w1=C.c_void_p((1 << 20) + 8)),
                 dict(w2=C.c_void_p((1 << 20) + 8)), dict(ws=C.c_void_p((1 << 20) + 8))):
         assert call(**bad) == L.MXQ_ERR_SHAPE, bad
