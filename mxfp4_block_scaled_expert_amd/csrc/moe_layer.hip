@@ -47,15 +47,6 @@ constexpr int kDownRows = 4;  // rows of an expert that one pass over its weight
 // were measured slower for one token and no faster for many: depths 3 / 4, 4 / 6, 8 / 6 of gate-up /
 // down took 35, 36, 41 us (one MXFP4 token) and 147, 147, 152 us (16 tokens).
 constexpr int kUpD = 3, kDownD = 4;
-constexpr int kDownRows = 4;  // rows of an expert that one pass over its weights takes in the down stage
-#ifndef UPD
-#define UPD 3
-#endif
-#ifndef DND
-#define DND 4
-#endif
-constexpr int kUpD = UPD;    // ring depth of the gate/up stream: 3 steps of 4 KB per wave in flight
-constexpr int kDownD = DND;  // of the down stream: 7 steps of 2 KB
 }  // namespace
 
 // ---------------------------------------------------------------- router product
