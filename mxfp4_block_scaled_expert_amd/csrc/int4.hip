@@ -27,6 +27,13 @@ namespace {
 
 constexpr int kI4Threads = 256;
 constexpr int kI4Stages = 3;
+constexpr int kI4DotRows = 4;
+#ifndef I4BIG
+#define I4BIG 128
+#endif
+constexpr int64_t kI4BigRows = I4BIG;
+constexpr int kI4Batch = 4, kI4MaxBatches = 16;
+constexpr int64_t kI4DotMaxK = 16384;  // eight waves of 64 blocks
 
 // Eight codes of a dword (element 0 in the lowest nibble) -> eight bf16 128 + q.
 __device__ __forceinline__ i32x4 decode8(uint32_t v) {
@@ -49,9 +56,163 @@ __device__ __forceinline__ i32x4 transpose_rows(const i32x4& d) {
   return i32x4{int(c[0]), int(c[1]), int(e[0]), int(e[1])};
 }
 
+// Scale i as loaded (bf16 bits or fp32 bits: nothing is done to it here, so no read has to be waited
+// for where it is requested), and its value.
+template <bool SBF>
+__device__ __forceinline__ uint32_t scale_bits(const void* s, int64_t i) {
+  return SBF ? uint32_t(reinterpret_cast<const uint16_t*>(s)[i]) : reinterpret_cast<const uint32_t*>(s)[i];
+}
+template <bool SBF>
+__device__ __forceinline__ float scale_value(uint32_t v) {
+  return __uint_as_float(SBF ? v << 16 : v);
+}
+
+// Two bf16 products added to c.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// The value of the lane N places on in this lane's row of 16.
+template <int N>
+__device__ __forceinline__ float rotate16(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, true));
+}
+
 }  // namespace
 
-template <int G, int MT, int CG>
+// ---------------------------------------------------------------- up to four rows: dot products
+
+// Few rows are bound by reading the weights once, and on one row tile of 16 most of the matrix
+// instruction's rows would be empty, so here a lane keeps 32 columns of every x row in registers
+// and takes the same 32 columns of weight rows (one 16-byte read each, whole 1 KB pieces of a row
+// per wave) through V_DOT2_F32_BF16.  Codes pair up four apart (code i and i + 4 of a dword sit 16
+// bits apart, so one AND-OR makes two bf16 of 128 + q), x is paired the same way once.  A lane's
+// columns lie in one group: its sum, less (128 + z) times its sum of x, times the scale, is what the
+// wave adds up.  A batch is four weight rows, the next batch's reads on their way while one is
+// computed; its sums are reduced over the lanes together, halving rows and lanes at once (permlane
+// swaps), and the KW waves of a workgroup, which split K, meet in LDS at the end.
+//
+// LPR lanes hold a row's share (64, or 32 / 16 where the share is that short: a read then covers
+// two / four rows).
+template <int M, int LPR, bool ZERO, bool SBF>
+__global__ __launch_bounds__(512) void int4_dot_kernel(Int4Args a, int kw, int bpw, int batches) {
+  constexpr int RB = kI4Batch, NI = RB * LPR / 64;  // rows of a batch, reads of a lane
+  __shared__ float part[8][RB * kI4MaxBatches][M];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rows = RB * batches;  // of this workgroup
+  const int64_t n0 = int64_t(blockIdx.x) * rows;
+  const int K = int(a.K), nblk = K / 32;
+  // this lane's block of 32 columns (past the wave's share: none, its x are zeros)
+  const int lb = lane & (LPR - 1), blk = wave * bpw + lb;
+  const bool on = lb < bpw && blk < nblk;
+  const int cb = on ? blk : 0;
+  const int gi = cb / (a.group / 32), ngrp = K / a.group, zrow = (ngrp + 1) / 2;
+  // the row of this lane's read i: the odd 16-lane rows and the upper half lanes further on where a
+  // read covers several
+  const int lrow = (LPR <= 32 ? (RB / 2) * (lane >> 5) : 0) + (LPR <= 16 ? (RB / 4) * ((lane >> 4) & 1) : 0);
+
+  struct Batch {
+    i32x4 w[NI];
+    uint32_t s[NI], z[NI];
+  };
+  auto load = [&](Batch& o, int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int64_t n = min<int64_t>(n0 + b * RB + lrow + i, a.N - 1);
+      o.w[i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(a.W + n * (K / 2) + cb * 16));
+      o.s[i] = scale_bits<SBF>(a.s, n * ngrp + gi);
+      if (ZERO) o.z[i] = a.z[n * zrow + (gi >> 1)];
+    }
+  };
+  Batch even, odd;
+  load(even, 0);
+  uint32_t x[M][16];
+  float xs[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const i32x4* xp = reinterpret_cast<const i32x4*>(reinterpret_cast<const uint16_t*>(a.A) + m * a.lda + cb * 32);
+    float t = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const i32x4 v = on ? xp[d] : i32x4{0, 0, 0, 0};
+      x[m][4 * d + 0] = __builtin_amdgcn_perm(uint32_t(v[2]), uint32_t(v[0]), 0x05040100u);
+      x[m][4 * d + 1] = __builtin_amdgcn_perm(uint32_t(v[2]), uint32_t(v[0]), 0x07060302u);
+      x[m][4 * d + 2] = __builtin_amdgcn_perm(uint32_t(v[3]), uint32_t(v[1]), 0x05040100u);
+      x[m][4 * d + 3] = __builtin_amdgcn_perm(uint32_t(v[3]), uint32_t(v[1]), 0x07060302u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = dot2(x[m][4 * d + j], 0x3f803f80u, t);
+    }
+    xs[m] = t;
+  }
+  auto compute = [&](const Batch& o, int b) __attribute__((always_inline)) {
+    float v[M][NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float acc[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) acc[m] = 0.f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t c = ((uint32_t(o.w[i][d]) >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+#pragma unroll
+          for (int m = 0; m < M; ++m) acc[m] = dot2(c, x[m][4 * d + j], acc[m]);
+        }
+      const float zc = ZERO ? float(128u + ((o.z[i] >> (4 * (gi & 1))) & 15u)) : 136.f, s = scale_value<SBF>(o.s[i]);
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m][i] = fmaf(-zc, xs[m], acc[m]) * s;
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if constexpr (LPR == 64) {
+#pragma unroll
+        for (int i = 0; i < RB / 2; ++i) {
+          const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[m][i]), __float_as_uint(v[m][i + RB / 2]), false, false);
+          v[m][i] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+        }
+      }
+      if constexpr (LPR >= 32) {
+#pragma unroll
+        for (int i = 0; i < RB / 4; ++i) {
+          const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[m][i]), __float_as_uint(v[m][i + RB / 4]), false, false);
+          v[m][i] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+        }
+      }
+      // the 16 lanes of a row: rotations by 8, 4, 2, 1
+#pragma unroll
+      for (int i = 0; i < RB / 4; ++i) {
+        v[m][i] += rotate16<8>(v[m][i]);
+        v[m][i] += rotate16<4>(v[m][i]);
+        v[m][i] += rotate16<2>(v[m][i]);
+        v[m][i] += rotate16<1>(v[m][i]);
+        // every lane of the row holds the sum of weight row i + RB / 4 * (odd row) + RB / 2 * (upper half)
+        if ((lane & 15) == i) part[wave][b * RB + i + RB / 4 * ((lane >> 4) & 1) + RB / 2 * (lane >> 5)][m] = v[m][i];
+      }
+    }
+  };
+  for (int b = 0; b < batches; b += 2) {
+    if (b + 1 < batches) load(odd, b + 1);
+    compute(even, b);
+    if (b + 2 < batches) load(even, b + 2);
+    if (b + 1 < batches) compute(odd, b + 1);
+  }
+  __syncthreads();
+  for (int c = tid; c < rows * M; c += blockDim.x) {
+    const int m = c / rows, r = c - m * rows;
+    const int64_t n = n0 + r;
+    if (n >= a.N) continue;
+    float t = 0.f;
+    for (int k = 0; k < kw; ++k) t += part[k][r][m];
+    if (a.bias)
+      t += a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n]) : reinterpret_cast<const float*>(a.bias)[n];
+    reinterpret_cast<uint16_t*>(a.out)[m * a.ldo + n] = f2bf(t);
+  }
+}
+
+// ---------------------------------------------------------------- more rows: matrix tiles
+
+template <int G, int MT, int CG, bool ZERO, bool SBF>
 __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
   constexpr int NS = kI4Stages, BM = 16 * MT, BN = 64 * CG, STAGE = BM * 256;
   constexpr int GPS = 128 / G;  // groups per step
@@ -109,9 +270,8 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
 #pragma unroll
       for (int j = 0; j < GPS; ++j) {
         const int g = min(st * GPS + j, ngrp - 1);
-        o.s[c][j] = a.s_bf16 ? uint32_t(reinterpret_cast<const uint16_t*>(a.s)[col[c] * ngrp + g])
-                             : reinterpret_cast<const uint32_t*>(a.s)[col[c] * ngrp + g];
-        o.z[c][j] = a.z ? uint32_t(a.z[col[c] * zrow + (g >> 1)]) : 0x88u;
+        o.s[c][j] = scale_bits<SBF>(a.s, col[c] * ngrp + g);
+        o.z[c][j] = ZERO ? uint32_t(a.z[col[c] * zrow + (g >> 1)]) : 0x88u;
       }
     }
   };
@@ -138,7 +298,7 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
       for (int c = 0; c < CG; ++c) {
 #pragma unroll
         for (int i = 0; i < MPG; ++i) bf[c][i] = decode8(uint32_t(wt[c][j * MPG + i]));
-        s[c] = a.s_bf16 ? bf16f(uint16_t(v.s[c][j])) : __uint_as_float(v.s[c][j]);
+        s[c] = scale_value<SBF>(v.s[c][j]);
         const int g = st * GPS + j;
         zc[c] = float(128u + ((v.z[c][j] >> (4 * (g & 1))) & 15u));
       }
@@ -211,13 +371,209 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
   }
 }
 
+// ---------------------------------------------------------------- many rows: large matrix tiles
+
+// A prompt is bound by the matrix instructions, so everything that is not one is taken out of the
+// loop: a pass over x first writes it with the eight columns of every 16-byte chunk in the order
+// 0 4 1 5 2 6 3 7 -- the order in which (v & 0x000f000f) | 0x43004300 and three shifts of it give
+// the codes of a dword, seven instructions for eight codes -- and the groups' sums X.  The
+// product of a group starts from -(128 + z) X, so what comes out is sum x (q - z).
+__global__ __launch_bounds__(256) void int4_prep_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t lda,
+                                                        int group, int64_t Mp, uint16_t* __restrict__ xp,
+                                                        float* __restrict__ X) {
+  const int64_t chunks = K / 8, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = i / chunks, c = i - m * chunks;
+  const int per = group / 8;  // chunks of a group: 4, 8 or 16 neighbouring lanes (rows are whole groups)
+  float t = 0.f;
+  if (m < M) {
+    const uint4 v = *reinterpret_cast<const uint4*>(x + m * lda + c * 8);
+    uint4 o;
+    o.x = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
+    o.y = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
+    o.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
+    o.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
+    *reinterpret_cast<uint4*>(xp + m * K + c * 8) = o;
+    t = dot2(o.x, 0x3f803f80u, dot2(o.y, 0x3f803f80u, dot2(o.z, 0x3f803f80u, dot2(o.w, 0x3f803f80u, 0.f))));
+  }
+  for (int o = 1; o < per; o <<= 1) t += __shfl_xor(t, o, kWave);
+  if (m < M && (c & (per - 1)) == 0) X[(c / per) * Mp + m] = t;
+}
+
+// BM = 256 rows x BN = 128 columns, eight waves of 64 x 64; lane l16 of column group c holds column
+// 4 l16 + c of its wave's 64, so a lane ends with four neighbouring columns of each of its rows.
+constexpr int kBigM = 256, kBigN = 128, kBigThreads = 512;
+
+template <int G, bool ZERO, bool SBF>
+__global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, const float* __restrict__ X, int64_t Mp) {
+  constexpr int GPS = 128 / G, MPG = G / 32, MT = 4, CG = 4;
+  constexpr int A_BYTES = kBigM * 256, STAGE = A_BYTES + GPS * kBigM * 4;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int wm = wave & 3, wn = wave >> 2;  // four waves along the rows, two along the columns
+  const int64_t n0 = int64_t(blockIdx.x) * kBigN, m0 = int64_t(blockIdx.y) * kBigM;
+  const int K = int(a.K), ngrp = K / G, zrow = (ngrp + 1) / 2, nsteps = (K + 127) / 128;
+
+  const uint32_t lds0 = lds_addr(smem);
+  const int r4 = lane >> 4, slot = lane & 15;
+  const int achunk = slot ^ ((wave * 4 + r4) & 15);  // (row % 16: 32 i drops out)
+  auto copy = [&](int st, int stage) __attribute__((always_inline)) {
+    int c = st * 128 + achunk * 8;
+    if (c >= K) c = 0;  // past the row's end: never multiplied
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = min<int64_t>(m0 + (i * 8 + wave) * 4 + r4, a.M - 1);
+      lds_dma16(reinterpret_cast<const uint16_t*>(a.A) + row * K + c, lds0 + uint32_t(stage * STAGE + (i * 8 + wave) * 1024));
+    }
+    if (wave < GPS)
+      lds_dma16(X + int64_t(min(st * GPS + wave, ngrp - 1)) * Mp + m0 + lane * 4,
+                lds0 + uint32_t(stage * STAGE + A_BYTES + wave * (kBigM * 4)));
+  };
+
+  auto col_of = [&](int c) __attribute__((always_inline)) { return min<int64_t>(n0 + wn * 64 + 4 * l16 + c, a.N - 1); };
+  struct Slot {
+    i32x4 w[CG];
+    uint32_t s[CG][GPS], z[CG][GPS];
+  } ring;
+  auto load = [&](int st) __attribute__((always_inline)) {
+    int b = st * 64 + q * 16;
+    if (b >= K / 2) b = 0;
+#pragma unroll
+    for (int c = 0; c < CG; ++c) {
+      const int64_t n = col_of(c);
+      ring.w[c] = *reinterpret_cast<const i32x4*>(a.W + n * (K / 2) + b);
+#pragma unroll
+      for (int j = 0; j < GPS; ++j) {
+        const int g = min(st * GPS + j, ngrp - 1);
+        ring.s[c][j] = scale_bits<SBF>(a.s, n * ngrp + g);
+        ring.z[c][j] = ZERO ? uint32_t(a.z[n * zrow + (g >> 1)]) : 0x88u;
+      }
+    }
+  };
+  f32x4 acc[MT][CG];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int c = 0; c < CG; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // One step.  Its codes are turned into bf16 in HALVES parts (a whole group at least); with the
+  // last of them taken, the next step's weights are requested into the same registers.
+  constexpr int HALVES = G == 128 ? 1 : 2, FR = 4 / HALVES, HG = GPS / HALVES;  // blocks, groups of a part
+  auto step = [&](int st, int stage) __attribute__((always_inline)) {
+    const uint8_t* as = smem + stage * STAGE + (wm * 64 + l16) * 256;
+    const uint8_t* xs = smem + stage * STAGE + A_BYTES + (wm * 64 + 4 * q) * 4;
+    const int blocks = min(4, (K - st * 128) / 32);
+    if (G < 128) {
+#pragma unroll
+      for (int c = 0; c < CG; ++c) ring.w[c] = transpose_rows(ring.w[c]);
+    }
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      i32x4 bf[CG][FR];
+      float s[CG][HG], zc[CG][HG];
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+#pragma unroll
+        for (int i = 0; i < FR; ++i) {
+          const uint32_t u = uint32_t(ring.w[c][h * FR + i]);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) bf[c][i][d] = int(((u >> (4 * d)) & 0x000f000fu) | 0x43004300u);
+        }
+#pragma unroll
+        for (int j = 0; j < HG; ++j) {
+          s[c][j] = scale_value<SBF>(ring.s[c][h * HG + j]);
+          zc[c][j] = -float(128u + ((ring.z[c][h * HG + j] >> (4 * ((st * GPS + h * HG + j) & 1))) & 15u));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (h == HALVES - 1 && st + 1 < nsteps) load(st + 1);
+#pragma unroll
+      for (int j = 0; j < HG; ++j) {
+        const int g = h * HG + j;  // of the step's groups
+        if (G < 128 && g * MPG >= blocks) break;  // uniform: past the row's end
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(xs + g * (kBigM * 4) + mt * 64);
+          f32x4 p[CG];
+#pragma unroll
+          for (int c = 0; c < CG; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[c][r] = zc[c][j] * x[r];
+#pragma unroll
+          for (int i = 0; i < MPG; ++i) {
+            const int chunk = G == 128 ? 4 * q + i : 4 * (g * MPG + i) + q;
+            const i32x4 af = *reinterpret_cast<const i32x4*>(as + mt * 16 * 256 + ((chunk ^ l16) * 16));
+#pragma unroll
+            for (int c = 0; c < CG; ++c) p[c] = mfma_16x16x32_bf16(af, bf[c][j * MPG + i], p[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < CG; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[mt][c][r] = fmaf(p[c][r], s[c][j], acc[mt][c][r]);
+          __builtin_amdgcn_sched_barrier(0x100);  // only LDS reads may move ahead: registers
+        }
+      }
+    }
+  };
+
+  copy(0, 0);
+  load(0);
+  for (int st = 0; st < nsteps; ++st) {
+    // a step's copies and weights were requested a whole step ago
+    wait_vmcnt<0>();
+    __syncthreads();
+    if (st + 1 < nsteps) copy(st + 1, (st + 1) & 1);
+    step(st, st & 1);
+  }
+
+  // ---- lane (l16, q): rows 4 q + r, columns 4 l16 .. + 4
+  const int64_t n = n0 + wn * 64 + 4 * l16;
+  float b[CG];
+#pragma unroll
+  for (int c = 0; c < CG; ++c)
+    b[c] = !a.bias ? 0.f
+                   : a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[col_of(c)])
+                                 : reinterpret_cast<const float*>(a.bias)[col_of(c)];
+  const bool whole = n + 4 <= a.N && (a.ldo & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t m = m0 + wm * 64 + mt * 16 + 4 * q + r;
+      if (m >= a.M) continue;
+      uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + m * a.ldo + n;
+      const uint32_t lo = pack_bf16x2(acc[mt][0][r] + b[0], acc[mt][1][r] + b[1]);
+      const uint32_t hi = pack_bf16x2(acc[mt][2][r] + b[2], acc[mt][3][r] + b[3]);
+      if (whole) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+      } else {
+        if (n + 0 < a.N) o[0] = uint16_t(lo);
+        if (n + 1 < a.N) o[1] = uint16_t(lo >> 16);
+        if (n + 2 < a.N) o[2] = uint16_t(hi);
+        if (n + 3 < a.N) o[3] = uint16_t(hi >> 16);
+      }
+    }
+}
+
 // ---------------------------------------------------------------- host side
+
+// GO(zero points given, bf16 scales)
+#define MXQ_I4_PICK(GO)                         \
+  do {                                          \
+    if (a.z && a.s_bf16) GO(true, true);        \
+    else if (a.z) GO(true, false);              \
+    else if (a.s_bf16) GO(false, true);         \
+    else GO(false, false);                      \
+  } while (0)
 
 namespace {
 template <int G, int MT, int CG>
 void launch_i4(const Int4Args& a, hipStream_t st) {
   const dim3 grid(unsigned(cdiv(a.N, 64 * CG)), unsigned(cdiv(a.M, 16 * MT)), unsigned(a.splits));
-  hipLaunchKernelGGL((int4_tile_kernel<G, MT, CG>), grid, dim3(kI4Threads), size_t(kI4Stages) * MT * 16 * 256, st, a);
+#define MXQ_I4(Z, S) \
+  hipLaunchKernelGGL((int4_tile_kernel<G, MT, CG, Z, S>), grid, dim3(kI4Threads), size_t(kI4Stages) * MT * 16 * 256, st, a)
+  MXQ_I4_PICK(MXQ_I4);
+#undef MXQ_I4
 }
 
 template <int G>
@@ -226,10 +582,65 @@ void launch_i4_g(const Int4Args& a, const Int4Plan& p, hipStream_t st) {
   else if (p.mt == 4) launch_i4<G, 4, 2>(a, st);
   else launch_i4<G, 8, 2>(a, st);
 }
+
+template <int G>
+void launch_i4_big(const Int4Args& a, const float* X, int64_t Mp, hipStream_t st) {
+  const dim3 grid(unsigned(cdiv(a.N, kBigN)), unsigned(cdiv(a.M, kBigM)));
+  const size_t lds = 2 * (size_t(kBigM) * 256 + (128 / G) * kBigM * 4);
+#define MXQ_I4(Z, S) hipLaunchKernelGGL((int4_big_kernel<G, Z, S>), grid, dim3(kBigThreads), lds, st, a, X, Mp)
+  MXQ_I4_PICK(MXQ_I4);
+#undef MXQ_I4
+}
+
+template <int M, int LPR>
+void launch_dot_z(const Int4Args& a, int kw, int bpw, int batches, hipStream_t st) {
+  const dim3 grid(unsigned(cdiv(a.N, kI4Batch * batches))), block(unsigned(64 * kw));
+#define MXQ_I4(Z, S) hipLaunchKernelGGL((int4_dot_kernel<M, LPR, Z, S>), grid, block, 0, st, a, kw, bpw, batches)
+  MXQ_I4_PICK(MXQ_I4);
+#undef MXQ_I4
+}
+
+template <int M>
+void launch_dot_l(const Int4Args& a, int kw, int bpw, int batches, hipStream_t st) {
+  if (bpw <= 16) launch_dot_z<M, 16>(a, kw, bpw, batches, st);
+  else if (bpw <= 32) launch_dot_z<M, 32>(a, kw, bpw, batches, st);
+  else launch_dot_z<M, 64>(a, kw, bpw, batches, st);
+}
+
+// Waves along K (64 blocks of 32 columns each at most), the blocks of a wave, and as many batches
+// per workgroup as leave 4096 waves for one row, 2048 for more (their registers leave room for
+// eight waves on a compute unit; 4096 x 16384 with groups of 64: one row 13.1 us against 16.5 with
+// 2048 waves and 26.7 with 1024, three rows 24.5, 19.0, 31.5 us).
+void launch_int4_dot(const Int4Args& a, hipStream_t st) {
+  const int nblk = int(a.K / 32);
+  const int kw = int(cdiv(nblk, 64)), bpw = int(cdiv(nblk, kw));
+  const int batches = int(std::max<int64_t>(1, std::min<int64_t>(kI4MaxBatches, a.N * kw / (kI4Batch * (a.M == 1 ? 4096 : 2048)))));
+  switch (a.M) {
+    case 1: launch_dot_l<1>(a, kw, bpw, batches, st); break;
+    case 2: launch_dot_l<2>(a, kw, bpw, batches, st); break;
+    case 3: launch_dot_l<3>(a, kw, bpw, batches, st); break;
+    default: launch_dot_l<4>(a, kw, bpw, batches, st); break;
+  }
+}
 }  // namespace
+
+// Workspace of the large tiles: x in its new order, then the groups' sums (of the smallest group,
+// whole row tiles).
+static size_t int4_big_x_bytes(int64_t M, int64_t K) { return (size_t(M) * size_t(K) * 2 + 255) & ~size_t(255); }
+static size_t int4_big_sums_bytes(int64_t M, int64_t K) {
+  return size_t(K / 32) * size_t(cdiv(M, kBigM) * kBigM) * 4;
+}
 
 Int4Plan int4_plan(int64_t M, int64_t N, int64_t K) {
   Int4Plan p{};
+  p.splits = 1;
+  p.split_steps = int32_t(cdiv(K, 128));
+  if (M <= kI4DotRows && K <= kI4DotMaxK) return p;
+  if (M >= kI4BigRows) {
+    p.mt = 16;
+    p.partial_bytes = int4_big_x_bytes(M, K) + int4_big_sums_bytes(M, K);
+    return p;
+  }
   p.mt = M <= 16 ? 1 : (M <= 64 ? 4 : 8);
   const int cg = p.mt == 1 ? 1 : 2;
   const int64_t tiles = cdiv(N, 64 * cg) * cdiv(M, 16 * p.mt), nsteps = cdiv(K, 128);
@@ -247,6 +658,24 @@ void launch_int4_linear(const Int4Args& g, int group, float* partial, hipStream_
   if (g.M <= 0 || g.N <= 0) return;
   const Int4Plan p = int4_plan(g.M, g.N, g.K);
   Int4Args a = g;
+  a.group = group;
+  if (p.mt == 0) {
+    launch_int4_dot(a, stream);
+    return;
+  }
+  if (p.mt == 16) {
+    uint16_t* xp = reinterpret_cast<uint16_t*>(partial);
+    float* X = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(partial) + int4_big_x_bytes(a.M, a.K));
+    const int64_t Mp = cdiv(a.M, kBigM) * kBigM;
+    const dim3 pg(unsigned(cdiv(a.M * (a.K / 8), 256)));
+    hipLaunchKernelGGL(int4_prep_kernel, pg, dim3(256), 0, stream, static_cast<const uint16_t*>(a.A), a.M, a.K, a.lda,
+                       group, Mp, xp, X);
+    a.A = xp;
+    if (group == 32) launch_i4_big<32>(a, X, Mp, stream);
+    else if (group == 64) launch_i4_big<64>(a, X, Mp, stream);
+    else launch_i4_big<128>(a, X, Mp, stream);
+    return;
+  }
   a.splits = p.splits;
   a.split_steps = p.split_steps;
   a.split_stride = g.M * g.N;

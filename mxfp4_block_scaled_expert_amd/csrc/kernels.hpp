@@ -322,11 +322,12 @@ struct Int4Args {
   void* out;                // bf16 [M, N], row stride ldo; K split: fp32 [splits][M][N]
   int64_t ldo;
   int64_t M, N, K;
+  int32_t group;
   int32_t splits, split_steps;  // K chunks of split_steps 128-wide steps
   int64_t split_stride;
 };
 struct Int4Plan {
-  int32_t mt;               // 16-row tiles per workgroup
+  int32_t mt;               // 16-row tiles per workgroup; 0: the dot-product kernel
   int32_t splits, split_steps;
   size_t partial_bytes;
 };
