@@ -590,12 +590,14 @@ mxq_status mxq_moe_layer_mxfp4(const void* x, int64_t M, int64_t H, int64_t I, i
  *            low nibble of byte j
  *   bias     NULL or [N] of bias_dtype (fp32 or bf16), added in fp32
  *   out      bf16 [M, N], row stride ldo elements (ldo >= N)
- *   workspace mxq_int4_linear_workspace_size(M, N, K) bytes (NULL allowed where it is 0): the fp32
- *            partial sums of a K split (added in chunk order; at most 16 MiB)
+ *   workspace mxq_int4_linear_workspace_size(M, N, K, group) bytes (NULL allowed where it is 0),
+ *            contents arbitrary: few tiles, the fp32 partial sums of a K split (added in chunk
+ *            order; at most 16 MiB); many rows, x reordered (2 M K bytes), its group sums and the
+ *            scales and zero points as pairs (8 N K / group bytes)
  *   fp32 sums; the scales multiply fp32 group sums, so the weights themselves are never rounded.
  *   w_scale, w_zero, bias and out need only their element's alignment.
  *   M <= 2^19, N and K <= 2^28; M == 0 or N == 0: no-op. */
-size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group);
 mxq_status mxq_int4_linear(const void* A, int64_t M, int64_t K, int64_t lda, const void* W, int64_t N, int32_t group,
                            const void* w_scale, int32_t scale_dtype, const void* w_zero, const void* bias,
                            int32_t bias_dtype, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,

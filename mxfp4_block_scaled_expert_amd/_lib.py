@@ -124,7 +124,7 @@ SIGNATURES = {
                                   _p, _p, _p, _i32, _p, _i64, _p, _sz, _p]),
     "mxq_moe_layer_mxfp4": (_i32, [_p, _i64, _i64, _i64, _i32, _i64, _p, _i32, _p, C.POINTER(MoeRouter), _p, _p, _p,
                                     _p, _p, _p, _i32, _p, _i64, _p, _sz, _p]),
-    "mxq_int4_linear_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "mxq_int4_linear_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "mxq_int4_linear": (_i32, [_p, _i64, _i64, _i64, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _p, _i64, _p, _sz,
                                 _p]),
 }

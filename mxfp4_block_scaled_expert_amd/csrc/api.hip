@@ -1598,9 +1598,9 @@ mxq_status mxq_moe_layer_mxfp4(const void* x, int64_t M, int64_t H, int64_t I, i
                    w2_scale, w1_bias, weight_layout, out, ldo, workspace, workspace_bytes, MXQ_WEIGHTS_MXFP4, stream);
 }
 
-size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return int4_plan(M, N, K).partial_bytes;
+size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group) {
+  if (M <= 0 || N <= 0 || K <= 0 || (group != 32 && group != 64 && group != 128) || K % group != 0) return 0;
+  return int4_plan(M, N, K, group).partial_bytes;
 }
 
 mxq_status mxq_int4_linear(const void* A, int64_t M, int64_t K, int64_t lda, const void* W, int64_t N, int32_t group,
@@ -1617,7 +1617,7 @@ mxq_status mxq_int4_linear(const void* A, int64_t M, int64_t K, int64_t lda, con
   if (K == 0) return MXQ_ERR_SHAPE;
   if (!A || !W || !w_scale || !out) return MXQ_ERR_NULL;
   if (!aligned16(A) || !aligned16(W)) return MXQ_ERR_SHAPE;
-  const size_t need = mxq_int4_linear_workspace_size(M, N, K);
+  const size_t need = mxq_int4_linear_workspace_size(M, N, K, group);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return MXQ_ERR_SHAPE;
   MXQ_TRY(check_arch());

@@ -15,7 +15,8 @@
 // its 16 CG columns.  Activations go through a ring of NS LDS stages (128 columns each, filled by
 // direct global-to-LDS copies, 16-byte chunks XOR-swizzled by row); weights, scales and zero
 // points go straight to registers, as many steps ahead.  Where tiles are few, K is cut into chunks
-// whose fp32 partial sums are added in chunk order by launch_dense_split_sum.
+// whose fp32 partial sums are added in chunk order by launch_dense_split_sum.  Up to four rows take
+// a dot-product kernel instead, prompts large tiles over x and scales laid out for them.
 #include <algorithm>
 
 #include "lds_dma.hpp"
@@ -28,10 +29,8 @@ namespace {
 constexpr int kI4Threads = 256;
 constexpr int kI4Stages = 3;
 constexpr int kI4DotRows = 4;
-#ifndef I4BIG
-#define I4BIG 128
-#endif
-constexpr int64_t kI4BigRows = I4BIG;
+// Large tiles: 32-bit offsets within a row tile, one thread per 16 bytes of x in one grid dimension.
+constexpr int64_t kI4BigMaxK = 1 << 22, kI4BigMaxX = int64_t(1) << 34;
 constexpr int kI4Batch = 4, kI4MaxBatches = 16;
 constexpr int64_t kI4DotMaxK = 16384;  // eight waves of 64 blocks
 
@@ -399,56 +398,75 @@ __global__ __launch_bounds__(256) void int4_prep_kernel(const uint16_t* __restri
   if (m < M && (c & (per - 1)) == 0) X[(c / per) * Mp + m] = t;
 }
 
+// The scales and zero points as the large tiles take them: (s, -(128 + z)) fp32 pairs, columns
+// neighbouring ([group][Np]), so that a step's arrive in LDS with one copy per group: gathered by every
+// wave from their rows, they were most of the loop's vector memory instructions.
+template <bool ZERO, bool SBF>
+__global__ __launch_bounds__(256) void int4_scale_prep_kernel(Int4Args a, int64_t Np, float2* __restrict__ sz) {
+  const int ngrp = int(a.K / a.group), zrow = (ngrp + 1) / 2;
+  const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= Np) return;
+  const int64_t nc = min<int64_t>(n, a.N - 1);
+  for (int g = int(blockIdx.y); g < ngrp; g += int(gridDim.y)) {
+    const float s = scale_value<SBF>(scale_bits<SBF>(a.s, nc * ngrp + g));
+    const uint32_t z = ZERO ? (uint32_t(a.z[nc * zrow + (g >> 1)]) >> (4 * (g & 1))) & 15u : 8u;
+    sz[int64_t(g) * Np + n] = make_float2(s, -float(128u + z));
+  }
+}
+
 // BM = 256 rows x BN = 128 columns, eight waves of 64 x 64; lane l16 of column group c holds column
 // 4 l16 + c of its wave's 64, so a lane ends with four neighbouring columns of each of its rows.
+// Measured: 2048 x 2048 -> 7168 in 107 / 112 / 135 us with groups of 128 / 64 / 32 (562 TFLOP/s with
+// 128, passes over x and the scales included; the 64 x 128 and 128 x 128 tiles take 130 / 218 / 316).
+// A step takes 2.5 to 3 us where its matrix instructions take 0.9: the two waves of a SIMD wait
+// for their weights and x together, LDS has no room for a second workgroup.
 constexpr int kBigM = 256, kBigN = 128, kBigThreads = 512;
 
-template <int G, bool ZERO, bool SBF>
-__global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, const float* __restrict__ X, int64_t Mp) {
+template <int G>
+__global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, const float* __restrict__ X, int64_t Mp,
+                                                                  const float2* __restrict__ sz, int64_t Np) {
   constexpr int GPS = 128 / G, MPG = G / 32, MT = 4, CG = 4;
-  constexpr int A_BYTES = kBigM * 256, STAGE = A_BYTES + GPS * kBigM * 4;
+  constexpr int A_BYTES = kBigM * 256, X_BYTES = GPS * kBigM * 4, STAGE = A_BYTES + X_BYTES + GPS * kBigN * 8;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
   const int wm = wave & 3, wn = wave >> 2;  // four waves along the rows, two along the columns
   const int64_t n0 = int64_t(blockIdx.x) * kBigN, m0 = int64_t(blockIdx.y) * kBigM;
-  const int K = int(a.K), ngrp = K / G, zrow = (ngrp + 1) / 2, nsteps = (K + 127) / 128;
+  const int K = int(a.K), ngrp = K / G, nsteps = (K + 127) / 128;
 
   const uint32_t lds0 = lds_addr(smem);
   const int r4 = lane >> 4, slot = lane & 15;
   const int achunk = slot ^ ((wave * 4 + r4) & 15);  // (row % 16: 32 i drops out)
+  // operands as a uniform base and 32-bit lane offsets (K <= 2^22, so 256 rows stay below 2^31 bytes)
+  const uint16_t* const ab = reinterpret_cast<const uint16_t*>(a.A) + m0 * K;
+  const int arows = int(min<int64_t>(a.M - m0, kBigM)), ncols = int(min<int64_t>(a.N - n0, kBigN));
   auto copy = [&](int st, int stage) __attribute__((always_inline)) {
     int c = st * 128 + achunk * 8;
     if (c >= K) c = 0;  // past the row's end: never multiplied
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = min<int64_t>(m0 + (i * 8 + wave) * 4 + r4, a.M - 1);
-      lds_dma16(reinterpret_cast<const uint16_t*>(a.A) + row * K + c, lds0 + uint32_t(stage * STAGE + (i * 8 + wave) * 1024));
-    }
-    if (wave < GPS)
-      lds_dma16(X + int64_t(min(st * GPS + wave, ngrp - 1)) * Mp + m0 + lane * 4,
-                lds0 + uint32_t(stage * STAGE + A_BYTES + wave * (kBigM * 4)));
+    for (int i = 0; i < 8; ++i)
+      lds_dma16(ab, uint32_t(min((i * 8 + wave) * 4 + r4, arows - 1) * K + c) * 2u,
+                lds0 + uint32_t(stage * STAGE + (i * 8 + wave) * 1024));
+    const int g = min(st * GPS + (wave & (GPS - 1)), ngrp - 1);
+    if (wave < GPS)  // 256 group sums; 128 scale and zero point pairs
+      lds_dma16(X + int64_t(g) * Mp + m0 + lane * 4, lds0 + uint32_t(stage * STAGE + A_BYTES + wave * (kBigM * 4)));
+    else if (wave < 2 * GPS)
+      lds_dma16(sz + int64_t(g) * Np + n0 + lane * 2,
+                lds0 + uint32_t(stage * STAGE + A_BYTES + X_BYTES + (wave - GPS) * (kBigN * 8)));
   };
 
-  auto col_of = [&](int c) __attribute__((always_inline)) { return min<int64_t>(n0 + wn * 64 + 4 * l16 + c, a.N - 1); };
+  const uint8_t* const wb = a.W + n0 * (K / 2);
+  int col[CG];  // from n0
+#pragma unroll
+  for (int c = 0; c < CG; ++c) col[c] = min(wn * 64 + 4 * l16 + c, ncols - 1);
   struct Slot {
     i32x4 w[CG];
-    uint32_t s[CG][GPS], z[CG][GPS];
-  } ring;
-  auto load = [&](int st) __attribute__((always_inline)) {
-    int b = st * 64 + q * 16;
-    if (b >= K / 2) b = 0;
+  };
+  auto load = [&](int st, Slot& o) __attribute__((always_inline)) {
+    uint32_t b = uint32_t(st * 64 + q * 16);
+    if (b >= uint32_t(K / 2)) b = 0;
 #pragma unroll
-    for (int c = 0; c < CG; ++c) {
-      const int64_t n = col_of(c);
-      ring.w[c] = *reinterpret_cast<const i32x4*>(a.W + n * (K / 2) + b);
-#pragma unroll
-      for (int j = 0; j < GPS; ++j) {
-        const int g = min(st * GPS + j, ngrp - 1);
-        ring.s[c][j] = scale_bits<SBF>(a.s, n * ngrp + g);
-        ring.z[c][j] = ZERO ? uint32_t(a.z[n * zrow + (g >> 1)]) : 0x88u;
-      }
-    }
+    for (int c = 0; c < CG; ++c) o.w[c] = *reinterpret_cast<const i32x4*>(wb + (uint32_t(col[c]) * uint32_t(K / 2) + b));
   };
   f32x4 acc[MT][CG];
 #pragma unroll
@@ -457,11 +475,12 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
     for (int c = 0; c < CG; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // One step.  Its codes are turned into bf16 in HALVES parts (a whole group at least); with the
-  // last of them taken, the next step's weights are requested into the same registers.
+  // last of them taken, the weights of two steps on are requested into the same registers.
   constexpr int HALVES = G == 128 ? 1 : 2, FR = 4 / HALVES, HG = GPS / HALVES;  // blocks, groups of a part
-  auto step = [&](int st, int stage) __attribute__((always_inline)) {
+  auto step = [&](int st, int stage, Slot& ring) __attribute__((always_inline)) {
     const uint8_t* as = smem + stage * STAGE + (wm * 64 + l16) * 256;
     const uint8_t* xs = smem + stage * STAGE + A_BYTES + (wm * 64 + 4 * q) * 4;
+    const uint8_t* ss = smem + stage * STAGE + A_BYTES + X_BYTES + (wn * 64 + 4 * l16) * 8;
     const int blocks = min(4, (K - st * 128) / 32);
     if (G < 128) {
 #pragma unroll
@@ -479,14 +498,17 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
 #pragma unroll
           for (int d = 0; d < 4; ++d) bf[c][i][d] = int(((u >> (4 * d)) & 0x000f000fu) | 0x43004300u);
         }
+      }
 #pragma unroll
-        for (int j = 0; j < HG; ++j) {
-          s[c][j] = scale_value<SBF>(ring.s[c][h * HG + j]);
-          zc[c][j] = -float(128u + ((ring.z[c][h * HG + j] >> (4 * ((st * GPS + h * HG + j) & 1))) & 15u));
-        }
+      for (int j = 0; j < HG; ++j) {
+        const f32x4 p0 = *reinterpret_cast<const f32x4*>(ss + (h * HG + j) * (kBigN * 8));
+        const f32x4 p1 = *reinterpret_cast<const f32x4*>(ss + (h * HG + j) * (kBigN * 8) + 16);
+        s[0][j] = p0[0]; zc[0][j] = p0[1]; s[1][j] = p0[2]; zc[1][j] = p0[3];
+        s[2][j] = p1[0]; zc[2][j] = p1[1]; s[3][j] = p1[2]; zc[3][j] = p1[3];
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (h == HALVES - 1 && st + 1 < nsteps) load(st + 1);
+      // (past the last step its weights are read again: the waits below count these reads)
+      if (h == HALVES - 1) load(min(st + 2, nsteps - 1), ring);
 #pragma unroll
       for (int j = 0; j < HG; ++j) {
         const int g = h * HG + j;  // of the step's groups
@@ -516,14 +538,21 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
     }
   };
 
+  Slot even, odd;
   copy(0, 0);
-  load(0);
-  for (int st = 0; st < nsteps; ++st) {
-    // a step's copies and weights were requested a whole step ago
-    wait_vmcnt<0>();
+  load(0, even);
+  load(min(1, nsteps - 1), odd);
+  for (int st = 0; st < nsteps; st += 2) {
+    // a step's copies were requested a step ago, and after them only the weights of a later step
+    wait_vmcnt<CG>();
     __syncthreads();
-    if (st + 1 < nsteps) copy(st + 1, (st + 1) & 1);
-    step(st, st & 1);
+    if (st + 1 < nsteps) copy(st + 1, 1);
+    step(st, 0, even);
+    if (st + 1 >= nsteps) break;
+    wait_vmcnt<CG>();
+    __syncthreads();
+    if (st + 2 < nsteps) copy(st + 2, 0);
+    step(st + 1, 1, odd);
   }
 
   // ---- lane (l16, q): rows 4 q + r, columns 4 l16 .. + 4
@@ -532,8 +561,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
 #pragma unroll
   for (int c = 0; c < CG; ++c)
     b[c] = !a.bias ? 0.f
-                   : a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[col_of(c)])
-                                 : reinterpret_cast<const float*>(a.bias)[col_of(c)];
+                   : a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n0 + col[c]])
+                                 : reinterpret_cast<const float*>(a.bias)[n0 + col[c]];
   const bool whole = n + 4 <= a.N && (a.ldo & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -584,12 +613,10 @@ void launch_i4_g(const Int4Args& a, const Int4Plan& p, hipStream_t st) {
 }
 
 template <int G>
-void launch_i4_big(const Int4Args& a, const float* X, int64_t Mp, hipStream_t st) {
+void launch_i4_big(const Int4Args& a, const float* X, int64_t Mp, const float2* sz, int64_t Np, hipStream_t st) {
   const dim3 grid(unsigned(cdiv(a.N, kBigN)), unsigned(cdiv(a.M, kBigM)));
-  const size_t lds = 2 * (size_t(kBigM) * 256 + (128 / G) * kBigM * 4);
-#define MXQ_I4(Z, S) hipLaunchKernelGGL((int4_big_kernel<G, Z, S>), grid, dim3(kBigThreads), lds, st, a, X, Mp)
-  MXQ_I4_PICK(MXQ_I4);
-#undef MXQ_I4
+  const size_t lds = 2 * (size_t(kBigM) * 256 + (128 / G) * (kBigM * 4 + kBigN * 8));
+  hipLaunchKernelGGL((int4_big_kernel<G>), grid, dim3(kBigThreads), lds, st, a, X, Mp, sz, Np);
 }
 
 template <int M, int LPR>
@@ -624,24 +651,45 @@ void launch_int4_dot(const Int4Args& a, hipStream_t st) {
 }
 }  // namespace
 
-// Workspace of the large tiles: x in its new order, then the groups' sums (of the smallest group,
-// whole row tiles).
-static size_t int4_big_x_bytes(int64_t M, int64_t K) { return (size_t(M) * size_t(K) * 2 + 255) & ~size_t(255); }
-static size_t int4_big_sums_bytes(int64_t M, int64_t K) {
-  return size_t(K / 32) * size_t(cdiv(M, kBigM) * kBigM) * 4;
+// Workspace of the large tiles: x in its new order, the groups' sums (whole row tiles), the scale and
+// zero point pairs (whole column tiles).
+struct BigWs {
+  int64_t Mp, Np;
+  size_t sums, pairs, total;
+};
+static BigWs int4_big_ws(int64_t M, int64_t N, int64_t K, int group) {
+  BigWs w;
+  w.Mp = cdiv(M, kBigM) * kBigM;
+  w.Np = cdiv(N, kBigN) * kBigN;
+  auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
+  w.sums = up(size_t(M) * size_t(K) * 2);
+  w.pairs = w.sums + up(size_t(K / group) * size_t(w.Mp) * 4);
+  w.total = w.pairs + size_t(K / group) * size_t(w.Np) * 8;
+  return w;
 }
 
-Int4Plan int4_plan(int64_t M, int64_t N, int64_t K) {
+Int4Plan int4_plan(int64_t M, int64_t N, int64_t K, int group) {
   Int4Plan p{};
   p.splits = 1;
   p.split_steps = int32_t(cdiv(K, 128));
   if (M <= kI4DotRows && K <= kI4DotMaxK) return p;
-  if (M >= kI4BigRows) {
+  // The large tiles, once they occupy three of four compute units, or half of them with groups below
+  // 128, which cost the other kernel one more product of ones each (us, large tiles against the others:
+  // 1024 x 2048 -> 7168, 224 tiles, 60 against 67 with groups of 128, 77 against 160 with 32;
+  // 1024 x 4096 -> 4096, 128 tiles, 103 against 66 and 126 against 154; 700 x 7168 -> 4096, 96 tiles,
+  // groups of 64, 170 against 172; 512 x 7168 -> 2048, 32 tiles, groups of 32, 207 against 88).
+  if (K <= kI4BigMaxK && M <= kI4BigMaxX / K && cdiv(M, kBigM) * cdiv(N, kBigN) >= (group == 128 ? 192 : 128)) {
     p.mt = 16;
-    p.partial_bytes = int4_big_x_bytes(M, K) + int4_big_sums_bytes(M, K);
+    p.partial_bytes = int4_big_ws(M, N, K, group).total;
     return p;
   }
-  p.mt = M <= 16 ? 1 : (M <= 64 ? 4 : 8);
+  // Rows of a tile (us with tiles of 16 x 64, 64 x 128, 128 x 128): few workgroups take longer than
+  // the weights read again -- 97 x 576 -> 224: 6.2, 15.8, 23.3; 32 x 7168 -> 2048: 16.1, 24.1, -;
+  // 64 x 7168 -> 2048: 14.8, 20.2, -; but 64 x 4096 -> 4096, groups of 32: 42.9, 30.0, -;
+  // 128 x 2048 -> 7168: 37.3, 29.9, 34.4; 512 x 2048 -> 2048: 37.5, 29.7, 33.9.
+  if (M <= 32 || cdiv(M, 16) * cdiv(N, 64) <= 128) p.mt = 1;
+  else if (M <= 64 || cdiv(M, 64) * cdiv(N, 128) <= 256) p.mt = 4;
+  else p.mt = 8;
   const int cg = p.mt == 1 ? 1 : 2;
   const int64_t tiles = cdiv(N, 64 * cg) * cdiv(M, 16 * p.mt), nsteps = cdiv(K, 128);
   int64_t s = 1;
@@ -656,7 +704,7 @@ Int4Plan int4_plan(int64_t M, int64_t N, int64_t K) {
 
 void launch_int4_linear(const Int4Args& g, int group, float* partial, hipStream_t stream) {
   if (g.M <= 0 || g.N <= 0) return;
-  const Int4Plan p = int4_plan(g.M, g.N, g.K);
+  const Int4Plan p = int4_plan(g.M, g.N, g.K, group);
   Int4Args a = g;
   a.group = group;
   if (p.mt == 0) {
@@ -664,16 +712,23 @@ void launch_int4_linear(const Int4Args& g, int group, float* partial, hipStream_
     return;
   }
   if (p.mt == 16) {
-    uint16_t* xp = reinterpret_cast<uint16_t*>(partial);
-    float* X = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(partial) + int4_big_x_bytes(a.M, a.K));
-    const int64_t Mp = cdiv(a.M, kBigM) * kBigM;
+    const BigWs w = int4_big_ws(a.M, a.N, a.K, group);
+    uint8_t* base = reinterpret_cast<uint8_t*>(partial);
+    uint16_t* xp = reinterpret_cast<uint16_t*>(base);
+    float* X = reinterpret_cast<float*>(base + w.sums);
+    float2* sz = reinterpret_cast<float2*>(base + w.pairs);
+    const int64_t Mp = w.Mp, Np = w.Np;
     const dim3 pg(unsigned(cdiv(a.M * (a.K / 8), 256)));
     hipLaunchKernelGGL(int4_prep_kernel, pg, dim3(256), 0, stream, static_cast<const uint16_t*>(a.A), a.M, a.K, a.lda,
                        group, Mp, xp, X);
     a.A = xp;
-    if (group == 32) launch_i4_big<32>(a, X, Mp, stream);
-    else if (group == 64) launch_i4_big<64>(a, X, Mp, stream);
-    else launch_i4_big<128>(a, X, Mp, stream);
+    const dim3 sg(unsigned(cdiv(Np, 256)), unsigned(std::min<int64_t>(a.K / group, 256)));
+#define MXQ_I4(Z, S) hipLaunchKernelGGL((int4_scale_prep_kernel<Z, S>), sg, dim3(256), 0, stream, a, Np, sz)
+    MXQ_I4_PICK(MXQ_I4);
+#undef MXQ_I4
+    if (group == 32) launch_i4_big<32>(a, X, Mp, sz, Np, stream);
+    else if (group == 64) launch_i4_big<64>(a, X, Mp, sz, Np, stream);
+    else launch_i4_big<128>(a, X, Mp, sz, Np, stream);
     return;
   }
   a.splits = p.splits;

@@ -331,7 +331,7 @@ struct Int4Plan {
   int32_t splits, split_steps;
   size_t partial_bytes;
 };
-Int4Plan int4_plan(int64_t M, int64_t N, int64_t K);
+Int4Plan int4_plan(int64_t M, int64_t N, int64_t K, int group);
 // group 32, 64 or 128; `partial`: int4_plan's partial_bytes of workspace
 void launch_int4_linear(const Int4Args& a, int group, float* partial, hipStream_t stream);
 

@@ -737,7 +737,7 @@ def int4_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     b = None if bias is None else bias.contiguous()
     out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     lib = L.load()
-    ws_bytes = lib.mxq_int4_linear_workspace_size(M, N, K)
+    ws_bytes = lib.mxq_int4_linear_workspace_size(M, N, K, K // groups)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
     st = lib.mxq_int4_linear(x2.data_ptr(), M, K, max(x2.stride(0), K), w.data_ptr(), N, K // groups, s.data_ptr(),
                              _LOGITS[s.dtype], _ptr(z), _ptr(b), _bias_dtype(b), out.data_ptr(), N, _ptr(ws), ws_bytes,

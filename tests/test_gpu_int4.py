@@ -142,7 +142,7 @@ def test_output_stride_leaves_the_rest_alone():
         w, s, z = (t.to(gpu()) for t in _weights(N, K, 64, 4))
         x = torch.randn(M, K, device=gpu()).to(torch.bfloat16)
         out = torch.full((M + 1, N + 5), 3.0, dtype=torch.bfloat16, device=gpu())
-        n = lib.mxq_int4_linear_workspace_size(M, N, K)
+        n = lib.mxq_int4_linear_workspace_size(M, N, K, 64)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=gpu())
         st = lib.mxq_int4_linear(x.data_ptr(), M, K, K, w.data_ptr(), N, 64, s.data_ptr(), L.MXQ_DTYPE_F32, z.data_ptr(),
                                  None, 0, out.data_ptr(), N + 5, ws.data_ptr(), n,
@@ -151,3 +151,88 @@ def test_output_stride_leaves_the_rest_alone():
         assert st == 0
         assert torch.equal(out[:M, :N], ops.int4_linear(x, w, s, z))
         assert (out[M:] == 3).all() and (out[:, N:] == 3).all()
+
+
+# whole and cut tiles of prompts: 2^17 .. 2^23 outputs, rows that end inside the 128-wide step
+PROMPTS = [(1000, 4100, 384), (700, 4100, 256), (1500, 4230, 512), (129, 16390, 640), (513, 6500, 1152), (257, 8300, 128)]
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", PROMPTS)
+def test_prompts_exact(M, N, K, G):
+    K = K if G == 128 else K - G
+    g = torch.Generator().manual_seed(M + N)
+    x = torch.randint(-4, 5, (M, K), generator=g).to(torch.bfloat16)
+    zero, sdtype = ((True, torch.float32), (False, torch.bfloat16), (True, torch.bfloat16))[(M + G) % 3]
+    w, s, z = _weights(N, K, G, N, zero, sdtype, pow2=True)
+    b = torch.randint(-8, 9, (N,), generator=g).to(sdtype) if zero else None
+    out = _run(x, w, s, z, b)
+    want = torch.from_numpy(_oracle(x, w, s, z, G, b)).to(torch.bfloat16)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,N,K,G", [(1025, 5000, 608, 32), (777, 9000, 1024, 128)])
+def test_prompts_random(M, N, K, G):
+    g = torch.Generator().manual_seed(N)
+    w, s, z = _weights(N, K, G, N, True, torch.bfloat16)
+    _check_random(torch.randn(M, K, generator=g).to(torch.bfloat16), w, s, z, G, torch.randn(N, generator=g))
+
+
+def test_prompt_rows_columns_and_strides():
+    """Rows keep their NaN to themselves, columns their scale's; strided x and out at an odd stride."""
+    lib = L.load()
+    M, N, K, G = 600, 6000, 256, 64
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(M, K + 8, generator=g).to(torch.bfloat16).to(gpu())
+    w, s, z = (t.to(gpu()) for t in _weights(N, K, G, 2))
+    ref = ops.int4_linear(x[:, :K], w, s, z)
+    assert torch.equal(ops.int4_linear(x[:, :K].contiguous(), w, s, z), ref)
+    n = lib.mxq_int4_linear_workspace_size(M, N, K, G)
+    assert n >= 2 * M * K  # x laid out for the large tiles
+    for ldo in (N, N + 1, N + 3):
+        out = torch.full((M + 1, ldo), 3.0, dtype=torch.bfloat16, device=gpu())
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device=gpu())  # NaN wherever it is read unwritten
+        st = lib.mxq_int4_linear(x.data_ptr(), M, K, K + 8, w.data_ptr(), N, G, s.data_ptr(), L.MXQ_DTYPE_F32,
+                                 z.data_ptr(), None, 0, out.data_ptr(), ldo, ws.data_ptr(), n,
+                                 torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(out[:M, :N], ref)
+        assert (out[M:] == 3).all() and (out[:, N:] == 3).all()
+    x[300, 7] = float("nan")
+    s[4000, 1] = float("nan")
+    bad = ops.int4_linear(x[:, :K], w, s, z)
+    rows, cols = torch.arange(M, device=gpu()) != 300, torch.arange(N, device=gpu()) != 4000
+    assert bad[300].isnan().all() and bad[:, 4000].isnan().all()
+    assert torch.equal(bad[rows][:, cols], ref[rows][:, cols])
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 300, 20480), (2, 64, 32768), (4, 40, 16384)])
+def test_few_rows_of_long_products(M, N, K):
+    """Up to four rows beyond the dot-product kernel's 16384 columns, and at that edge."""
+    g = torch.Generator().manual_seed(K)
+    w, s, z = _weights(N, K, 64, K, True, torch.float32)
+    _check_random(torch.randn(M, K, generator=g).to(torch.bfloat16), w, s, z, 64)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 512, 2048), (16, 512, 8192), (1030, 4100, 256)])
+def test_captured_graph_and_other_stream(M, N, K):
+    """One captured call, replayed with eager calls of other inputs between, and the same on a side stream."""
+    g = torch.Generator().manual_seed(M)
+    w, s, z = (t.to(gpu()) for t in _weights(N, K, 64, 3, True, torch.bfloat16))
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(gpu())
+    ops.int4_linear(x, w, s, z)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ops.int4_linear(x, w, s, z)
+    for i in range(4):
+        x.copy_(torch.randn(M, K, generator=g).to(torch.bfloat16))
+        graph.replay()
+        want = ops.int4_linear(x, w, s, z)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = ops.int4_linear(x, w, s, z)
+    side.synchronize()
+    assert torch.equal(other, want)

@@ -105,10 +105,11 @@ def test_int4_refusals():
         assert call(**{name: None}) == L.MXQ_ERR_NULL, name
     assert call(M=0) == L.MXQ_OK and call(N=0) == L.MXQ_OK
     q = LIB.mxq_int4_linear_workspace_size
-    assert q(0, 64, 256) == 0 and q(4096, 4096, 4096) == 0
-    for M, N, K in ((16, 2048, 7168), (128, 512, 8192), (64, 64, 16384)):
-        n = q(M, N, K)
-        assert n % (4 * M * N) == 0 and n <= 16 << 20
+    assert q(0, 64, 256, 64) == 0 and q(4, 64, 256, 48) == 0 and q(4, 64, 224, 64) == 0 and q(4, 2048, 7168, 64) == 0
+    assert q(4096, 4096, 4096, 128) >= 2 * 4096 * 4096
+    for M, N, K in ((16, 2048, 7168), (64, 64, 16384), (2048, 512, 8192)):
+        n = q(M, N, K, 64)
+        assert M > 64 or (n % (4 * M * N) == 0 and n <= 16 << 20)
         if n:
             assert call(M=M, N=N, K=K, lda=K, ldo=N, ws=None) == L.MXQ_ERR_WORKSPACE
             assert call(M=M, N=N, K=K, lda=K, ldo=N, n=n - 1) == L.MXQ_ERR_WORKSPACE
