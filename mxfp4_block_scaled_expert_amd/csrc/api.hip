@@ -8,6 +8,7 @@
 
 #include "../../include/mxq.h"
 #include "kernels.hpp"
+#include "layer.hpp"
 
 using namespace mxq;
 

@@ -19,8 +19,8 @@
 // a dot-product kernel instead, prompts large tiles over x and scales laid out for them.
 #include <algorithm>
 
+#include "layer.hpp"
 #include "lds_dma.hpp"
-#include "kernels.hpp"
 
 namespace mxq {
 

@@ -34,7 +34,7 @@
 // hi and lo are simply two rows of the same product.
 #include <algorithm>
 
-#include "kernels.hpp"
+#include "layer.hpp"
 #include "route_common.hpp"
 
 namespace mxq {

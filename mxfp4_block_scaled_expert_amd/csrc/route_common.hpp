@@ -14,7 +14,7 @@
 // of the lanes' best picks, and the lowest lane that holds it is the lowest index.
 #pragma once
 
-#include "kernels.hpp"
+#include "layer.hpp"
 
 namespace mxq {
 
@@ -46,26 +46,64 @@ __device__ __forceinline__ float wave_total(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// The same for 64-bit values, as two 32-bit moves a step (through LDS shuffles a routing in 64 bits
+// took 9 us more).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_d(double old, double v) {
+  const int lo = __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), CTRL, ROWS, 0xf, false);
+  return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double lane_value(double v, int src) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), src),
+                          __builtin_amdgcn_readlane(__double2loint(v), src));
+}
+
 __device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, kWave));
-  return v;
+  v = fmax(v, dpp_d<0x111, 0xf>(v, v));
+  v = fmax(v, dpp_d<0x112, 0xf>(v, v));
+  v = fmax(v, dpp_d<0x114, 0xf>(v, v));
+  v = fmax(v, dpp_d<0x118, 0xf>(v, v));
+  v = fmax(v, dpp_d<0x142, 0xa>(v, v));
+  v = fmax(v, dpp_d<0x143, 0xc>(v, v));
+  return lane_value(v, 63);
 }
 
 __device__ __forceinline__ double wave_total(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  v += dpp_d<0x111, 0xf>(0., v);
+  v += dpp_d<0x112, 0xf>(0., v);
+  v += dpp_d<0x114, 0xf>(0., v);
+  v += dpp_d<0x118, 0xf>(0., v);
+  v += dpp_d<0x142, 0xa>(0., v);
+  v += dpp_d<0x143, 0xc>(0., v);
+  return lane_value(v, 63);
 }
 
 // Lane `src`'s value (src uniform) in every lane.
 __device__ __forceinline__ float lane_value(float v, int src) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
 }
-__device__ __forceinline__ double lane_value(double v, int src) { return __shfl(v, src, kWave); }
 
 __device__ __forceinline__ float route_exp(float x) { return expf(x); }
 __device__ __forceinline__ double route_exp(double x) { return exp(x); }
+
+// The distance two fp32 picks must have to be told apart: p is within 1e-6 of itself, a sum of two
+// within its rounding.
+template <typename T>
+__device__ __forceinline__ bool route_near(T x, T y) {
+  return x - y <= T(6e-6) + T(5e-7) * (fabs(x) + fabs(y));
+}
+
+// A chosen expert's score relative to that of the largest chosen logit m, which is what
+// renormalising divides.  softmax: exp(l - m).  sigmoid: exp(-log(1 + exp(-l))) relative to m's, so
+// that tiny scores keep their ratio.
+template <typename T>
+__device__ __forceinline__ T route_ratio(float l, float m, int sigmoid) {
+  if (l == m) return T(1);
+  if (sigmoid && m > 0.f) return (T(1) + route_exp(-T(m))) / (T(1) + route_exp(-T(l)));
+  const T ratio = route_exp(T(l) - T(m));  // exp(l) / exp(m)
+  return sigmoid ? ratio * (T(1) + route_exp(T(m))) / (T(1) + route_exp(T(l))) : ratio;
+}
 
 // What lane k < topk holds after a routing: slot k's expert (-1: none) and weight.
 struct RouteSlot {
@@ -121,9 +159,6 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
     const T v = by_score ? p[i] + T(b[i]) : T(l[i]);
     pick[i] = live[i] && v > kNone ? v : kNone;  // (a NaN bias takes its expert out too)
   }
-  // the distance two fp32 picks must have to be told apart: p is within 1e-6 of itself, a sum of
-  // two within its rounding
-  auto near = [&](T x, T y) { return x - y <= T(6e-6) + T(5e-7) * (fabs(x) + fabs(y)); };
   close = false;
 
   // ---- groups
@@ -140,6 +175,7 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
     if (lane < a.n_group) {
       T m1 = kNone, m2 = kNone;
       const T* v = s_val + lane * a.group_size;
+#pragma unroll 8  // reads in flight together
       for (int j = 0; j < a.group_size; ++j) {
         const T x = v[j];
         m2 = fmax(m2, fmin(m1, x));
@@ -153,7 +189,7 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
       const T mx = wave_max(gs);
       if (!(mx > kNone)) break;
       if (r == a.topk_group) {
-        if (F32 && (by_score || a.group_top2)) close = close || near(last, mx);
+        if (F32 && (by_score || a.group_top2)) close = close || route_near(last, mx);
         break;
       }
       const int g = __builtin_ctzll(__ballot(gs == mx));
@@ -185,7 +221,7 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
       }
     const T mx = wave_max(best);
     if (!(mx > kNone)) break;
-    if (watch && k > 0) close = close || near(last, mx);
+    if (watch && k > 0) close = close || route_near(last, mx);
     last = mx;
     if (k == a.topk) break;
     const int win = __builtin_ctzll(__ballot(best == mx));
@@ -214,17 +250,8 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
 
   // ---- weights
   if (a.renormalize) {
-    // softmax: exp(l - m) / sum with m the largest chosen logit.  sigmoid: the same with
-    // sigmoid(l) = exp(-log(1 + exp(-l))), taken relative to the largest chosen one so that tiny
-    // scores keep their ratio
     const float m = wave_max(my_l);
-    T v = T(0);
-    if (out.id >= 0) {
-      const T ratio = my_l == m ? T(1) : route_exp(T(my_l) - T(m));  // exp(l) / exp(m)
-      v = ratio;
-      if (a.sigmoid) v = my_l == m ? T(1) : ratio * (T(1) + route_exp(T(m))) / (T(1) + route_exp(T(my_l)));
-      if (a.sigmoid && m > 0.f) v = (T(1) + route_exp(-T(m))) / (T(1) + route_exp(-T(my_l)));
-    }
+    const T v = out.id >= 0 ? route_ratio<T>(my_l, m, a.sigmoid) : T(0);
     const T tot = wave_total(v);
     out.w = out.id >= 0 ? float(v / tot) * a.scale : 0.f;
   } else {

@@ -23,6 +23,7 @@ from __future__ import annotations
 from typing import Dict, NamedTuple, Optional, Sequence, Tuple
 
 import ctypes
+import functools
 
 import torch
 
@@ -549,9 +550,8 @@ class Router(NamedTuple):
     scale: float = 1.0
 
 
-def _router(r: Router):
-    if not isinstance(r, Router):
-        raise ValueError(f"router must be a Router, got {type(r).__name__}")
+@functools.lru_cache(maxsize=256)
+def _router_struct(r: Router):
     if r.scoring not in _SCORING:
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {r.scoring!r}")
     if r.group_score not in _GROUP_SCORE:
@@ -560,15 +560,26 @@ def _router(r: Router):
                                     _GROUP_SCORE[r.group_score], int(bool(r.renormalize)), float(r.scale)))
 
 
-def _one_device(x: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
-    """Every tensor on x's GPU, and that GPU the current one (kernels run on its current stream)."""
+def _router(r: Router):
+    if not isinstance(r, Router):
+        raise ValueError(f"router must be a Router, got {type(r).__name__}")
+    return _router_struct(r)
+
+
+# A call of few tokens is over in microseconds, so its checks are made of the cheap questions: a
+# tensor's device number, the raw handle of a device's stream (0.1 us; as objects 0.5 and 1.5 us).
+
+def _one_device(x: torch.Tensor, *ts: Optional[torch.Tensor]) -> int:
+    """The current stream of x's GPU, where every tensor has to be; that GPU has to be the current one."""
     if not x.is_cuda:
         raise ValueError("all tensors must be on the GPU")
+    dev = x.get_device()
     for t in ts:
-        if t is not None and t.device != x.device:
+        if t is not None and (t.get_device() != dev or not t.is_cuda):
             raise ValueError(f"all tensors must be on {x.device}, got one on {t.device}")
-    if x.device.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _vector(t: Optional[torch.Tensor], n: int, name: str) -> Optional[torch.Tensor]:
@@ -599,21 +610,25 @@ def moe_route(logits: torch.Tensor, router: Router, correction_bias: Optional[to
     M, E = logits.shape
     r = _router(router)
     bias = _vector(correction_bias, E, "correction_bias")
-    _one_device(logits, bias)
+    stream = _one_device(logits, bias)
     if logits.stride(1) != 1 or (M > 1 and logits.stride(0) < E):
         logits = logits.contiguous()
-    ids = torch.empty((M, router.topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((M, router.topk), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((M, router.topk), dtype=torch.int32)
+    weights = logits.new_empty((M, router.topk), dtype=torch.float32)
     st = L.load().mxq_moe_route(logits.data_ptr(), _LOGITS[logits.dtype], M, E, max(logits.stride(0), E), r,
-                                _ptr(bias), ids.data_ptr(), weights.data_ptr(), _stream())
+                                _ptr(bias), ids.data_ptr(), weights.data_ptr(), stream)
     L.check("mxq_moe_route", st)
     return ids, weights
 
 
+@functools.lru_cache(maxsize=1024)
+def _layer_bytes(M: int, H: int, I: int, E: int, topk: int, weights: int) -> int:
+    return L.load().mxq_moe_layer_workspace_size(M, H, I, E, topk, weights)
+
+
 def moe_layer_workspace(M: int, H: int, I: int, E: int, topk: int, weights: int, device) -> torch.Tensor:
     """Workspace of a ``moe_layer_*`` call (``weights``: MXQ_WEIGHTS_*); its contents do not matter."""
-    n = L.load().mxq_moe_layer_workspace_size(M, H, I, E, topk, weights)
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    return torch.empty(max(_layer_bytes(M, H, I, E, topk, weights), 1), dtype=torch.uint8, device=device)
 
 
 def _moe_layer(name, weights, x, gate, router, w1, s1, w2, s2, w1_bias, gate_bias, correction_bias, workspace, out,
@@ -622,30 +637,30 @@ def _moe_layer(name, weights, x, gate, router, w1, s1, w2, s2, w1_bias, gate_bia
     E, two_i, h1 = w1.shape
     I = two_i // 2
     r = _router(router)
-    if gate.dtype not in _LOGITS or tuple(gate.shape) != (E, H):
+    if gate.dtype not in _LOGITS or gate.shape != (E, H):
         raise ValueError(f"gate must be fp32 or bf16 [{E}, {H}]")
-    if two_i % 2 or h1 != rb1 or tuple(w2.shape) != (E, H, rb2):
+    if two_i % 2 or h1 != rb1 or w2.shape != (E, H, rb2):
         raise ValueError(f"w1 must be [E, 2I, {rb1}] and w2 [E, H, {rb2}] in this layout")
-    if tuple(s1.shape) != shape_s1 or tuple(s2.shape) != shape_s2:
+    if s1.shape != shape_s1 or s2.shape != shape_s2:
         raise ValueError(f"scales must be {list(shape_s1)} and {list(shape_s2)} in this layout")
     if M > 16:
         raise ValueError(f"at most 16 tokens, got {M}: moe_route and the fused MoE take more")
     b1 = _vector(w1_bias, E * two_i, "w1_bias")
     gb = _vector(gate_bias, E, "gate_bias")
     cb = _vector(correction_bias, E, "correction_bias")
-    _one_device(x, gate, w1, s1, w2, s2, b1, gb, cb, workspace, out)
+    stream = _one_device(x, gate, w1, s1, w2, s2, b1, gb, cb, workspace, out)
     x = _rows(x)
     gate = gate.contiguous()
     if out is None:
-        out = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, H) or out.stride(1) != 1 or (M > 1 and out.stride(0) < H):
+        out = x.new_empty((M, H))
+    elif out.dtype != torch.bfloat16 or out.shape != (M, H) or out.stride(1) != 1 or (M > 1 and out.stride(0) < H):
         raise ValueError(f"out must be bf16 [{M}, {H}] with whole rows")
     if workspace is None:
         workspace = moe_layer_workspace(M, H, I, E, router.topk, weights, x.device)
     st = getattr(L.load(), name)(x.data_ptr(), M, H, I, E, max(x.stride(0), H), gate.data_ptr(), _LOGITS[gate.dtype],
                                  _ptr(gb), r, _ptr(cb), w1.data_ptr(), s1.data_ptr(), w2.data_ptr(), s2.data_ptr(),
                                  _ptr(b1), layout, out.data_ptr(), max(out.stride(0), H), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream())
+                                 workspace.numel() * workspace.element_size(), stream)
     L.check(name, st)
     return out
 
@@ -705,6 +720,11 @@ def moe_layer_mxfp4(x: torch.Tensor, gate: torch.Tensor, router: Router, w1: tor
 
 # ----------------------------------------------------------------------- 4-bit weights, group scales
 
+@functools.lru_cache(maxsize=1024)
+def _int4_bytes(M: int, N: int, K: int, group: int) -> int:
+    return L.load().mxq_int4_linear_workspace_size(M, N, K, group)
+
+
 def int4_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
                 weight_zero: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """4-bit linear with group scales: bf16 [..., K] @ ((q - z) * s)^T (+ bias) -> bf16 [..., N].
@@ -725,22 +745,21 @@ def int4_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     if groups == 0 or K % groups or K // groups not in (32, 64, 128):
         raise ValueError(f"weight_scale has {groups} groups for K {K}: the group must be 32, 64 or 128")
     if weight_zero is not None and (weight_zero.dtype != torch.uint8 or
-                                    tuple(weight_zero.shape) != (N, -(-groups // 2))):
+                                    weight_zero.shape != (N, -(-groups // 2))):
         raise ValueError(f"weight_zero must be packed uint8 [{N}, {-(-groups // 2)}]")
     if bias is not None and bias.numel() != N:
         raise ValueError("bias must have N elements")
-    _one_device(x, weight, weight_scale, weight_zero, bias)
-    x2 = _rows(x.reshape(-1, K))
+    stream = _one_device(x, weight, weight_scale, weight_zero, bias)
+    x2 = _rows(x if x.dim() == 2 else x.reshape(-1, K))
     M = x2.shape[0]
     w, s = weight.contiguous(), weight_scale.contiguous()
     z = None if weight_zero is None else weight_zero.contiguous()
     b = None if bias is None else bias.contiguous()
-    out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    lib = L.load()
-    ws_bytes = lib.mxq_int4_linear_workspace_size(M, N, K, K // groups)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
-    st = lib.mxq_int4_linear(x2.data_ptr(), M, K, max(x2.stride(0), K), w.data_ptr(), N, K // groups, s.data_ptr(),
-                             _LOGITS[s.dtype], _ptr(z), _ptr(b), _bias_dtype(b), out.data_ptr(), N, _ptr(ws), ws_bytes,
-                             _stream())
+    out = x2.new_empty((M, N))
+    ws_bytes = _int4_bytes(M, N, K, K // groups)
+    ws = x2.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
+    st = L.load().mxq_int4_linear(x2.data_ptr(), M, K, max(x2.stride(0), K), w.data_ptr(), N, K // groups, s.data_ptr(),
+                                  _LOGITS[s.dtype], _ptr(z), _ptr(b), _bias_dtype(b), out.data_ptr(), N, _ptr(ws), ws_bytes,
+                                  stream)
     L.check("mxq_int4_linear", st)
-    return out.view(*x.shape[:-1], N)
+    return out if x.dim() == 2 else out.view(*x.shape[:-1], N)

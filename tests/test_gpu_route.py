@@ -153,3 +153,55 @@ def test_rows_behind_the_last_are_left_alone():
                                 w.data_ptr(), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert st == 0 and (ids[5:] == -7).all() and (w[5:] == -7).all() and (ids[:5] >= 0).all()
+
+
+@pytest.mark.parametrize("M,E,router", [
+    (2049, 256, R(8, scoring="sigmoid", n_group=8, topk_group=4, group_score="top2", renormalize=True, scale=2.5)),
+    (1027, 64, R(16, renormalize=True)), (1500, 60, R(6, scoring="sigmoid")), (1025, 3, R(3)),
+    (1030, 128, R(4, scoring="sigmoid", renormalize=True)), (1201, 128, R(6, n_group=4, topk_group=2)),
+    (1100, 257, R(7)), (1040, 512, R(8, n_group=2, topk_group=1, group_score="top2")), (1090, 510, R(17)),
+    (1111, 160, R(6, n_group=8, topk_group=3)), (1033, 64, R(3, scoring="sigmoid", n_group=16, topk_group=5)),
+    (1029, 40, R(3, n_group=5, topk_group=2, group_score="top2")), (1031, 20, R(2, n_group=5, topk_group=5))])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens(M, E, router, with_bias, dtype):
+    g = torch.Generator().manual_seed(E)
+    bias = torch.randn(E, generator=g) * 0.1 if with_bias else None
+    l = _logits(M, E, M + E, dtype)
+    l[5] = -math.inf
+    l[6] = math.nan
+    l[7, 1:] = -math.inf
+    l[8] = 0.0
+    l[9, E // 2:] = -math.inf
+    l[M - 1, 0] = math.inf
+    l[M - 2] = torch.finfo(dtype).min
+    _check(l, router, bias)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_many_tokens_ties_and_close_picks(scoring):
+    g = torch.Generator().manual_seed(2)
+    l = torch.randint(-2, 3, (1100, 96), generator=g).float()
+    for r in (R(6, scoring=scoring), R(6, scoring=scoring, n_group=8, topk_group=3, group_score="top2"),
+              R(6, scoring=scoring, n_group=4, topk_group=2)):
+        _check(l, r)
+        _check(l, r, torch.full((96,), 0.25))
+    # half of the tokens have scores + bias nearer to each other than fp32 scores resolve
+    one = _logits(1, 64, 40)
+    p = torch.softmax(one.double(), 1) if scoring == "softmax" else torch.sigmoid(one.double())
+    l = torch.cat([one.expand(600, 64), _logits(600, 64, 41)])[torch.randperm(1200, generator=g)].contiguous()
+    for r in (R(8, scoring=scoring), R(8, scoring=scoring, n_group=8, topk_group=3, group_score="top2")):
+        _check(l, r, (0.7 - p[0]).float())
+
+
+def test_many_tokens_strides():
+    wide = _logits(1100, 200, 3).to(gpu())
+    for r in (R(4), R(4, n_group=5, topk_group=2)):
+        for view in (wide[:, 7:107], wide[:, 8:108], wide[1:, :100]):  # unaligned and aligned rows
+            a, b = ops.moe_route(view, r), ops.moe_route(view.contiguous(), r)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        # the same tokens in a call of few
+        few = ops.moe_route(wide[:40, :100], r)
+        many = ops.moe_route(wide[:, :100], r)
+        assert torch.equal(few[0], many[0][:40])
+        torch.testing.assert_close(few[1], many[1][:40], rtol=2 * RTOL, atol=0)
