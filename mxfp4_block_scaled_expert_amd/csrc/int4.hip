@@ -416,17 +416,22 @@ __global__ __launch_bounds__(256) void int4_scale_prep_kernel(Int4Args a, int64_
 
 // BM = 256 rows x BN = 128 columns, eight waves of 64 x 64; lane l16 of column group c holds column
 // 4 l16 + c of its wave's 64, so a lane ends with four neighbouring columns of each of its rows.
-// Measured: 2048 x 2048 -> 7168 in 107 / 112 / 135 us with groups of 128 / 64 / 32 (562 TFLOP/s with
-// 128, passes over x and the scales included; the 64 x 128 and 128 x 128 tiles take 130 / 218 / 316).
-// A step takes 2.5 to 3 us where its matrix instructions take 0.9: the two waves of a SIMD wait
-// for their weights and x together, LDS has no room for a second workgroup.
+// A stage holds x, codes, group sums and pairs, all copied by DMA a step ahead: 148 to 160 KB for
+// two.  (Codes straight to registers, read by each of the four waves that use them, took 107 us
+// where this takes 92.)
+// Measured: 2048 x 2048 -> 7168 in 92 / 110 / 131 us with groups of 128 / 64 / 32, the passes over x
+// and the scales included (128: 655 TFLOP/s); the 64 x 128 and 128 x 128 tiles take 130 / 218 / 316.
+// Nothing bounds it alone: a step takes 2.4 us, its matrix instructions 0.9; without the copies it
+// is 14 % shorter, without three of four matrix instructions 10 %, without the scales' arithmetic
+// 9 %.  The two waves of a SIMD pass the same barrier and so wait together.
 constexpr int kBigM = 256, kBigN = 128, kBigThreads = 512;
 
 template <int G>
 __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, const float* __restrict__ X, int64_t Mp,
                                                                   const float2* __restrict__ sz, int64_t Np) {
   constexpr int GPS = 128 / G, MPG = G / 32, MT = 4, CG = 4;
-  constexpr int A_BYTES = kBigM * 256, X_BYTES = GPS * kBigM * 4, STAGE = A_BYTES + X_BYTES + GPS * kBigN * 8;
+  constexpr int A_BYTES = kBigM * 256, W_BYTES = kBigN * 64, X_BYTES = GPS * kBigM * 4;
+  constexpr int W_AT = A_BYTES, X_AT = W_AT + W_BYTES, S_AT = X_AT + X_BYTES, STAGE = S_AT + GPS * kBigN * 8;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
@@ -440,51 +445,48 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
   // operands as a uniform base and 32-bit lane offsets (K <= 2^22, so 256 rows stay below 2^31 bytes)
   const uint16_t* const ab = reinterpret_cast<const uint16_t*>(a.A) + m0 * K;
   const int arows = int(min<int64_t>(a.M - m0, kBigM)), ncols = int(min<int64_t>(a.N - n0, kBigN));
+  // weights: LDS row 16 (4 wn + c) + l16 is column 64 wn + 4 l16 + c of the tile, its four 16-byte
+  // chunks XOR-swizzled by l16 / 4; wave w copies LDS rows [16 w, +16)
+  const uint8_t* const wb = a.W + n0 * (K / 2);
+  const uint32_t wrow = uint32_t(min((wave >> 2) * 64 + 4 * r4 * 4 + (slot >> 2) * 4 + (wave & 3), ncols - 1)) * uint32_t(K / 2);
+  const int wchunk = (slot & 3) ^ r4;
   auto copy = [&](int st, int stage) __attribute__((always_inline)) {
     int c = st * 128 + achunk * 8;
     if (c >= K) c = 0;  // past the row's end: never multiplied
+    uint32_t b = uint32_t(st * 64 + wchunk * 16);
+    if (b >= uint32_t(K / 2)) b = 0;
+    lds_dma16(wb, wrow + b, lds0 + uint32_t(stage * STAGE + W_AT + wave * 1024));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       lds_dma16(ab, uint32_t(min((i * 8 + wave) * 4 + r4, arows - 1) * K + c) * 2u,
                 lds0 + uint32_t(stage * STAGE + (i * 8 + wave) * 1024));
     const int g = min(st * GPS + (wave & (GPS - 1)), ngrp - 1);
     if (wave < GPS)  // 256 group sums; 128 scale and zero point pairs
-      lds_dma16(X + int64_t(g) * Mp + m0 + lane * 4, lds0 + uint32_t(stage * STAGE + A_BYTES + wave * (kBigM * 4)));
+      lds_dma16(X + int64_t(g) * Mp + m0 + lane * 4, lds0 + uint32_t(stage * STAGE + X_AT + wave * (kBigM * 4)));
     else if (wave < 2 * GPS)
       lds_dma16(sz + int64_t(g) * Np + n0 + lane * 2,
-                lds0 + uint32_t(stage * STAGE + A_BYTES + X_BYTES + (wave - GPS) * (kBigN * 8)));
+                lds0 + uint32_t(stage * STAGE + S_AT + (wave - GPS) * (kBigN * 8)));
   };
 
-  const uint8_t* const wb = a.W + n0 * (K / 2);
-  int col[CG];  // from n0
-#pragma unroll
-  for (int c = 0; c < CG; ++c) col[c] = min(wn * 64 + 4 * l16 + c, ncols - 1);
-  struct Slot {
-    i32x4 w[CG];
-  };
-  auto load = [&](int st, Slot& o) __attribute__((always_inline)) {
-    uint32_t b = uint32_t(st * 64 + q * 16);
-    if (b >= uint32_t(K / 2)) b = 0;
-#pragma unroll
-    for (int c = 0; c < CG; ++c) o.w[c] = *reinterpret_cast<const i32x4*>(wb + (uint32_t(col[c]) * uint32_t(K / 2) + b));
-  };
   f32x4 acc[MT][CG];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int c = 0; c < CG; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // One step.  Its codes are turned into bf16 in HALVES parts (a whole group at least); with the
-  // last of them taken, the weights of two steps on are requested into the same registers.
+  // One step.  Its codes are turned into bf16 in HALVES parts (a whole group at least).
   constexpr int HALVES = G == 128 ? 1 : 2, FR = 4 / HALVES, HG = GPS / HALVES;  // blocks, groups of a part
-  auto step = [&](int st, int stage, Slot& ring) __attribute__((always_inline)) {
+  auto step = [&](int st, int stage) __attribute__((always_inline)) {
+    const uint8_t* ws = smem + stage * STAGE + W_AT + wn * 4096 + l16 * 64 + ((q ^ (l16 >> 2)) * 16);
     const uint8_t* as = smem + stage * STAGE + (wm * 64 + l16) * 256;
-    const uint8_t* xs = smem + stage * STAGE + A_BYTES + (wm * 64 + 4 * q) * 4;
-    const uint8_t* ss = smem + stage * STAGE + A_BYTES + X_BYTES + (wn * 64 + 4 * l16) * 8;
+    const uint8_t* xs = smem + stage * STAGE + X_AT + (wm * 64 + 4 * q) * 4;
+    const uint8_t* ss = smem + stage * STAGE + S_AT + (wn * 64 + 4 * l16) * 8;
     const int blocks = min(4, (K - st * 128) / 32);
-    if (G < 128) {
+    i32x4 w[CG];
 #pragma unroll
-      for (int c = 0; c < CG; ++c) ring.w[c] = transpose_rows(ring.w[c]);
+    for (int c = 0; c < CG; ++c) {
+      w[c] = *reinterpret_cast<const i32x4*>(ws + c * 1024);
+      if (G < 128) w[c] = transpose_rows(w[c]);
     }
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
@@ -494,7 +496,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
       for (int c = 0; c < CG; ++c) {
 #pragma unroll
         for (int i = 0; i < FR; ++i) {
-          const uint32_t u = uint32_t(ring.w[c][h * FR + i]);
+          const uint32_t u = uint32_t(w[c][h * FR + i]);
 #pragma unroll
           for (int d = 0; d < 4; ++d) bf[c][i][d] = int(((u >> (4 * d)) & 0x000f000fu) | 0x43004300u);
         }
@@ -506,9 +508,6 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
         s[0][j] = p0[0]; zc[0][j] = p0[1]; s[1][j] = p0[2]; zc[1][j] = p0[3];
         s[2][j] = p1[0]; zc[2][j] = p1[1]; s[3][j] = p1[2]; zc[3][j] = p1[3];
       }
-      __builtin_amdgcn_sched_barrier(0);
-      // (past the last step its weights are read again: the waits below count these reads)
-      if (h == HALVES - 1) load(min(st + 2, nsteps - 1), ring);
 #pragma unroll
       for (int j = 0; j < HG; ++j) {
         const int g = h * HG + j;  // of the step's groups
@@ -532,27 +531,17 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
           for (int c = 0; c < CG; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[mt][c][r] = fmaf(p[c][r], s[c][j], acc[mt][c][r]);
-          __builtin_amdgcn_sched_barrier(0x100);  // only LDS reads may move ahead: registers
         }
       }
     }
   };
 
-  Slot even, odd;
   copy(0, 0);
-  load(0, even);
-  load(min(1, nsteps - 1), odd);
-  for (int st = 0; st < nsteps; st += 2) {
-    // a step's copies were requested a step ago, and after them only the weights of a later step
-    wait_vmcnt<CG>();
-    __syncthreads();
-    if (st + 1 < nsteps) copy(st + 1, 1);
-    step(st, 0, even);
-    if (st + 1 >= nsteps) break;
-    wait_vmcnt<CG>();
-    __syncthreads();
-    if (st + 2 < nsteps) copy(st + 2, 0);
-    step(st + 1, 1, odd);
+  for (int st = 0; st < nsteps; ++st) {
+    wait_vmcnt<0>();  // this step's copies, requested a step ago
+    __syncthreads();  // and everyone's; the other stage has been read
+    if (st + 1 < nsteps) copy(st + 1, (st + 1) & 1);
+    step(st, st & 1);
   }
 
   // ---- lane (l16, q): rows 4 q + r, columns 4 l16 .. + 4
@@ -561,8 +550,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
 #pragma unroll
   for (int c = 0; c < CG; ++c)
     b[c] = !a.bias ? 0.f
-                   : a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n0 + col[c]])
-                                 : reinterpret_cast<const float*>(a.bias)[n0 + col[c]];
+                   : a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n0 + min(wn * 64 + 4 * l16 + c, ncols - 1)])
+                                 : reinterpret_cast<const float*>(a.bias)[n0 + min(wn * 64 + 4 * l16 + c, ncols - 1)];
   const bool whole = n + 4 <= a.N && (a.ldo & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -615,7 +604,7 @@ void launch_i4_g(const Int4Args& a, const Int4Plan& p, hipStream_t st) {
 template <int G>
 void launch_i4_big(const Int4Args& a, const float* X, int64_t Mp, const float2* sz, int64_t Np, hipStream_t st) {
   const dim3 grid(unsigned(cdiv(a.N, kBigN)), unsigned(cdiv(a.M, kBigM)));
-  const size_t lds = 2 * (size_t(kBigM) * 256 + (128 / G) * (kBigM * 4 + kBigN * 8));
+  const size_t lds = 2 * (size_t(kBigM) * 256 + kBigN * 64 + (128 / G) * (kBigM * 4 + kBigN * 8));
   hipLaunchKernelGGL((int4_big_kernel<G>), grid, dim3(kBigThreads), lds, st, a, X, Mp, sz, Np);
 }
 
