@@ -236,3 +236,20 @@ def test_captured_graph_and_other_stream(M, N, K):
         other = ops.int4_linear(x, w, s, z)
     side.synchronize()
     assert torch.equal(other, want)
+
+
+@pytest.mark.parametrize("G", [32, 64])
+@pytest.mark.parametrize("sdtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(9, 70, 640), (40, 140, 256), (700, 4100, 384)])
+def test_scales_and_zero_points_at_odd_addresses(M, N, K, G, sdtype):
+    """Scales and zero points one element behind an aligned address give what aligned ones give."""
+    g = torch.Generator().manual_seed(N)
+    w, s, z = (t.to(gpu()) for t in _weights(N, K, G, 6, True, sdtype))
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(gpu())
+    want = ops.int4_linear(x, w, s, z)
+    s1 = torch.empty(s.numel() + 1, dtype=sdtype, device=gpu())[1:].view(s.shape)
+    z1 = torch.empty(z.numel() + 1, dtype=torch.uint8, device=gpu())[1:].view(z.shape)
+    s1.copy_(s)
+    z1.copy_(z)
+    for ss, zz in ((s1, z), (s, z1), (s1, z1)):
+        assert torch.equal(ops.int4_linear(x, w, ss, zz), want)
