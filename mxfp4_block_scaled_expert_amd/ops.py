@@ -566,8 +566,9 @@ def _router(r: Router):
     return _router_struct(r)
 
 
-# A call of few tokens is over in microseconds, so its checks are made of the cheap questions: a
-# tensor's device number, the raw handle of a device's stream (0.1 us; as objects 0.5 and 1.5 us).
+# A call of few tokens is over in microseconds, so its checks are made of the cheap questions -- a
+# tensor's device number, the raw handle of a device's stream -- and what follows from sizes alone is
+# kept (a 4-bit linear of one row costs the host 9.5 us so, 16 us with device and stream objects).
 
 def _one_device(x: torch.Tensor, *ts: Optional[torch.Tensor]) -> int:
     """The current stream of x's GPU, where every tensor has to be; that GPU has to be the current one."""
