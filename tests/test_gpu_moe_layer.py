@@ -96,6 +96,23 @@ def test_mxfp4_ragged_steps(M, H, I):
     check(make(True, M, 6, H, I, seed=H + I), R(2, renormalize=True))
 
 
+@pytest.mark.parametrize("M,H,I", [(1, 64, 64), (2, 2880, 192), (5, 320, 2880), (16, 448, 1088)])
+def test_mxfp4_scale_codes_in_pairs(M, H, I):
+    """Multiples of 64 that end inside a step; codes that differ between neighbouring groups; codes at an
+    odd address."""
+    d = make(True, M, 6, H, I, seed=H + I)
+    g = torch.Generator().manual_seed(H)
+    for k in ("w1_scale", "w2_scale"):
+        d[k] = torch.randint(116, 124, d[k].shape, generator=g, dtype=torch.uint8)
+    r = R(2, renormalize=True)
+    out, _ = check(d, r)
+    o = on_gpu(d)
+    for k in ("w1_scale", "w2_scale"):
+        odd = torch.empty(o[k].numel() + 1, dtype=torch.uint8, device=gpu())[1:].view(o[k].shape)
+        odd.copy_(o[k])
+        assert torch.equal(call(dict(o, **{k: odd}), r), out)
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_many_batches_of_rows(mx):
     """16 tokens on the same two experts, and on all of many: row batches that cut experts, batches
