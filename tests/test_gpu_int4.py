@@ -253,3 +253,22 @@ def test_scales_and_zero_points_at_odd_addresses(M, N, K, G, sdtype):
     z1.copy_(z)
     for ss, zz in ((s1, z), (s, z1), (s1, z1)):
         assert torch.equal(ops.int4_linear(x, w, ss, zz), want)
+
+
+def test_three_streams_at_once():
+    """Each form on a stream of its own, at once with the others: their workspaces are their own."""
+    calls = []
+    for M, N, K in ((3, 512, 4096), (16, 512, 8192), (1030, 4100, 256)):
+        g = torch.Generator().manual_seed(M)
+        w, s, z = (t.to(gpu()) for t in _weights(N, K, 64, M, True, torch.bfloat16))
+        calls.append((torch.randn(M, K, generator=g).to(torch.bfloat16).to(gpu()), w, s, z))
+    want = [ops.int4_linear(*c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    outs = [[] for _ in calls]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(ops.int4_linear(*calls[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(3) for o in outs[i])
