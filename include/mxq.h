@@ -552,7 +552,7 @@ mxq_status mxq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, in
 /* ------------------------------------------------------------------ whole MoE layer, few tokens
  * Router product, routing, expert products and combine of at most 16 tokens in one call:
  *   logits = x @ gate^T + gate_bias            (fp32 sums)
- *   (ids, w) = the routing above
+ *   (ids, w) = the routing above of these fp32 logits, near picks in 64 bits included
  *   g, u = x[t] @ w1[e]^T + w1_bias[e]  (rows [0, I) of w1 the gate, [I, 2I) the up projection)
  *   out[t] = bf16( sum_j (w[t, j] * silu(g) * u) @ w2[ids[t, j]]^T )
  * Weights, scales, bias and layouts are those of mxq_fused_moe_fp8 (with bf16 activations) and

@@ -129,9 +129,10 @@ __device__ __forceinline__ UpTables up_tables(uint8_t* p, int E, int R) {
 }
 
 // Routes the pass's tokens and groups their rows by expert.  Every thread of the workgroup calls
-// it; `scratch`: E floats per wave where the router has groups.
+// it; `scratch`: E doubles per wave (read where the router has groups).  As in moe_route_kernel, a token
+// with picks too close for fp32 scores is routed again in 64 bits, on the same fp32 logits.
 template <int KPL>
-__device__ __forceinline__ void build_tables(const LayerArgs& a, const UpTables& T, float* scratch) {
+__device__ __forceinline__ void build_tables(const LayerArgs& a, const UpTables& T, double* scratch) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = a.rt.E, topk = a.rt.topk, M = a.M, R = M * topk;
   for (int e = tid; e < E; e += kLyThreads) T.mask[e] = 0;
@@ -164,7 +165,11 @@ __device__ __forceinline__ void build_tables(const LayerArgs& a, const UpTables&
         for (int i = 0; i < KPL; ++i) l[i] += v[c][i];
     }
     bool close;
-    const RouteSlot s = route_token<KPL, float>(l, b, a.rt, scratch + wave * E, close);
+    RouteSlot s = route_token<KPL, float>(l, b, a.rt, reinterpret_cast<float*>(scratch + wave * E), close);
+    if (__builtin_expect(close, 0)) {  // (with the hint one token's layer takes 0.2 us more than without the repeat, 0.6 us else)
+      bool unused;
+      s = route_token<KPL, double>(l, b, a.rt, scratch + wave * E, unused);
+    }
     if (lane < topk) {
       T.id[t * topk + lane] = s.id;
       T.w[t * topk + lane] = s.w;
@@ -507,7 +512,7 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
       if (c < valid) v = *reinterpret_cast<const i32x4*>(a.x + (t + a.t0) * a.ldx + c * 8);
       *reinterpret_cast<i32x4*>(xs + t * stride + c * 16) = v;
     }
-  build_tables<KPL>(a, T, reinterpret_cast<float*>(xs + a.M * stride));
+  build_tables<KPL>(a, T, reinterpret_cast<double*>(xs + a.M * stride));
   if (blockIdx.x == 0) {  // for the down stage
     const int rows = T.misc[0];
     for (int j = tid; j < rows; j += kLyThreads) a.rows[1 + j] = T.row[j];
@@ -845,12 +850,11 @@ int layer_cus() {
 }
 
 // the shares of items (2 x 16 x 16 fp32 per wave), or before them the routing's group scratch
-// (E <= 512 floats per wave)
-constexpr uint32_t kUpScratch = kLyWaves * 2 * 256 * 4;
-static_assert(kUpScratch >= kLyWaves * kRouteMaxExperts * 4, "group scratch");
+// (E doubles per wave)
+uint32_t up_scratch(int E) { return std::max(uint32_t(kLyWaves * 2 * 256 * 4), uint32_t(kLyWaves * E * 8)); }
 
 uint32_t up_lds(bool mx, int64_t H, int E, int topk, int M) {
-  return up_table_bytes(E, M * topk) + uint32_t(M) * layer_row_stride(mx, int(H)) + kUpScratch;
+  return up_table_bytes(E, M * topk) + uint32_t(M) * layer_row_stride(mx, int(H)) + up_scratch(E);
 }
 
 uint32_t down_lds(bool mx, int R) {

@@ -262,3 +262,41 @@ def test_decode_step_of_all_three_operators():
     for k in (0, 1):
         for v in outs[k]:
             assert torch.equal(v.view(torch.int16), refs[k].view(torch.int16))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("E,case", [(32, "saturated"), (64, "near"), (300, "saturated"), (512, "near"), (8, "near")])
+def test_picks_closer_than_fp32_scores(mx, E, case):
+    """Scores + bias that fp32 cannot tell apart choose the experts that moe_route chooses.  Token t's x
+    is the t-th unit vector, so its logits are the router's t-th column, exact in fp32 in any order of
+    summation.  saturated: sigmoids of logits in [17, 28], 1 - e^-17 at least, all 1 in fp32, largest
+    logits last.  near: biases that leave only their own fp32 rounding between the picks."""
+    M, H = 5, 256
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn(M, E, generator=g)
+    bias = torch.zeros(E)
+    if case == "saturated":
+        n = E // 2
+        logits[:, E - n:] = torch.sort(torch.rand(M, n, generator=g) * 11 + 17, dim=1)[0]
+    else:
+        logits = logits[:1].expand(M, E).contiguous()
+    routers = [R(4, scoring="sigmoid", renormalize=True)]
+    if E > 8:
+        routers += [R(6, scoring="sigmoid", n_group=4, topk_group=2, group_score="top2")]
+    if case == "near":
+        routers += [R(4)]
+    for r in routers:
+        d = make(mx, M, E, H, 128, seed=E, gate_dtype=torch.float32)
+        d["x"] = torch.eye(M, H).to(torch.bfloat16)
+        d["gate"] = torch.zeros(E, H)
+        d["gate"][:, :M] = logits.t()
+        if case == "near":
+            p = torch.softmax(logits[0].double(), 0) if r.scoring == "softmax" else torch.sigmoid(logits[0].double())
+            bias = (0.7 - p).float()
+        d["bias"] = bias
+        want, bound, ids, _ = oracle(d, r)
+        routed, _ = ops.moe_route(logits.to(gpu()), r, correction_bias=bias.to(gpu()))
+        np.testing.assert_array_equal(routed.cpu().numpy(), ids)
+        for lay in ("plain", "tiled"):
+            got = call(on_gpu(d, lay), r, lay).double().cpu().numpy()
+            assert (np.abs(got - want) <= HALF * np.abs(want) + bound).all(), (lay, r)
