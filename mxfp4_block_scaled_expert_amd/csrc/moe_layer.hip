@@ -51,6 +51,12 @@ constexpr int kUpD = 3, kDownD = 4;
 
 // ---------------------------------------------------------------- router product
 
+// Two bf16 with infinities and NaNs replaced by zeros.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  const uint32_t lo = (v & 0x7f80u) == 0x7f80u ? 0u : 0xffffu, hi = (v & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+  return v & (lo | hi);
+}
+
 // part[s][t][e]: the sum over K chunk s.  Grid: (ceil(E / 16), S); the four waves of a workgroup
 // take the chunk's 32-wide steps in turn.
 template <bool F32W>
@@ -70,7 +76,11 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_kernel(const uint16_t* 
       const float* gp = reinterpret_cast<const float*>(gate) + grow + k;
       const f32x4 g0 = *reinterpret_cast<const f32x4*>(gp), g1 = *reinterpret_cast<const f32x4*>(gp + 4);
       float v[8] = {g0[0], g0[1], g0[2], g0[3], g1[0], g1[1], g1[2], g1[3]};
-      // v = t0 + t1 + t2 with bf16 terms: each term takes the next eight bits of the significand
+      // v = t0 + t1 + t2 with bf16 terms: each term takes the next eight bits of the significand.  An
+      // infinite activation meets only the first, which has v's sign: the others' are any, or zero.
+      i32x4 fin;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fin[i] = int(finite_bf16x2(uint32_t(af[i])));
 #pragma unroll
       for (int term = 0; term < 3; ++term) {
         i32x4 b;
@@ -83,7 +93,7 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_kernel(const uint16_t* 
           v[2 * i] = fabsf(lo) < __builtin_huge_valf() ? v[2 * i] - lo : 0.f;
           v[2 * i + 1] = fabsf(hi) < __builtin_huge_valf() ? v[2 * i + 1] - hi : 0.f;
         }
-        acc = mfma_16x16x32_bf16(af, b, acc);
+        acc = mfma_16x16x32_bf16(term == 0 ? af : fin, b, acc);
       }
     } else {
       const i32x4 bf = *reinterpret_cast<const i32x4*>(reinterpret_cast<const uint16_t*>(gate) + grow + k);

@@ -300,3 +300,33 @@ def test_picks_closer_than_fp32_scores(mx, E, case):
         for lay in ("plain", "tiled"):
             got = call(on_gpu(d, lay), r, lay).double().cpu().numpy()
             assert (np.abs(got - want) <= HALF * np.abs(want) + bound).all(), (lay, r)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_infinite_activation_with_fp32_router(mx):
+    """An infinite activation makes its token's logits +-inf by the sign of the router's weight there, with
+    an fp32 router as with a bf16 one: the experts of +inf are chosen, and what they make of an infinity
+    is no number -- while no expert (zeros) is only right where every logit is -inf."""
+    d = make(mx, 6, 8, 256, 128, seed=21, gate_dtype=torch.float32)
+    d["gate"][:, 70] = torch.tensor([1.1, -0.9, 1.3, -1.7, 0.7, -0.3, 2.9, -1.0])
+    d["gate"][:, 71] = -d["gate"][:, 70].abs()
+    r = R(2, renormalize=True)
+    o = on_gpu(d)
+    base = call(o, r)
+    x = o["x"].clone()
+    x[1, 70] = math.inf    # four experts of +inf
+    x[2, 70] = -math.inf   # the other four
+    x[3, 71] = math.inf    # none
+    x[4, 71] = -math.inf   # all
+    for gate in (o["gate"], o["gate"].to(torch.bfloat16)):
+        out = call(dict(o, gate=gate), r, x=x)
+        assert out[[1, 2, 4]].isnan().all() and (out[3] == 0).all()
+        assert out[[0, 5]].isfinite().all()
+    assert torch.equal(call(o, r, x=x)[[0, 5]], base[[0, 5]])
+    # the product itself: one expert, whose weight's terms differ in sign; -inf leaves none
+    one = make(mx, 2, 1, 256, 128, seed=22, gate_dtype=torch.float32)
+    one["x"][:, 9] = math.inf
+    for w, dead in ((1.0 + 2.0 ** -8 - 2.0 ** -20, False), (-1.0 - 2.0 ** -8 + 2.0 ** -20, True), (1.0, False)):
+        one["gate"][0, 9] = w
+        out = call(on_gpu(one), R(1))
+        assert (out == 0).all() if dead else out.isnan().all(), w
