@@ -75,9 +75,11 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_kernel(const uint16_t* 
     if constexpr (F32W) {
       const float* gp = reinterpret_cast<const float*>(gate) + grow + k;
       const f32x4 g0 = *reinterpret_cast<const f32x4*>(gp), g1 = *reinterpret_cast<const f32x4*>(gp + 4);
+      const float v0[8] = {g0[0], g0[1], g0[2], g0[3], g1[0], g1[1], g1[2], g1[3]};
       float v[8] = {g0[0], g0[1], g0[2], g0[3], g1[0], g1[1], g1[2], g1[3]};
-      // v = t0 + t1 + t2 with bf16 terms: each term takes the next eight bits of the significand.  An
-      // infinite activation meets only the first, which has v's sign: the others' are any, or zero.
+      // v = t0 + t1 + t2 with bf16 terms: each term cuts off the next eight bits of the significand (cut, not
+      // rounded: a weight above bf16's largest finite value would round to infinity).  An infinite
+      // activation meets only the first, which has v's sign: the others may be zero.
       i32x4 fin;
 #pragma unroll
       for (int i = 0; i < 4; ++i) fin[i] = int(finite_bf16x2(uint32_t(af[i])));
@@ -86,12 +88,22 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_kernel(const uint16_t* 
         i32x4 b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-          b[i] = int(w);
-          // (an infinite or NaN weight has no remainder)
-          const float lo = bf16lo(w), hi = bf16hi(w);
-          v[2 * i] = fabsf(lo) < __builtin_huge_valf() ? v[2 * i] - lo : 0.f;
-          v[2 * i + 1] = fabsf(hi) < __builtin_huge_valf() ? v[2 * i + 1] - hi : 0.f;
+          uint32_t lo = __float_as_uint(v[2 * i]) & 0xffff0000u, hi = __float_as_uint(v[2 * i + 1]) & 0xffff0000u;
+          v[2 * i] -= __uint_as_float(lo);
+          v[2 * i + 1] -= __uint_as_float(hi);
+          if (term == 0) {
+            // an infinite or NaN weight stays what it is and has no remainder
+            const uint32_t w = pack_bf16x2(v0[2 * i], v0[2 * i + 1]);
+            if (!(fabsf(v0[2 * i]) < __builtin_huge_valf())) {
+              lo = w << 16;
+              v[2 * i] = 0.f;
+            }
+            if (!(fabsf(v0[2 * i + 1]) < __builtin_huge_valf())) {
+              hi = w & 0xffff0000u;
+              v[2 * i + 1] = 0.f;
+            }
+          }
+          b[i] = int(hi | lo >> 16);
         }
         acc = mfma_16x16x32_bf16(term == 0 ? af : fin, b, acc);
       }

@@ -330,3 +330,27 @@ def test_infinite_activation_with_fp32_router(mx):
         one["gate"][0, 9] = w
         out = call(on_gpu(one), R(1))
         assert (out == 0).all() if dead else out.isnan().all(), w
+
+
+def test_fp32_router_weights_above_bf16():
+    """fp32 router weights beyond bf16's largest finite value stay finite; infinite and NaN ones do what they
+    do in a bf16 router."""
+    d = make(False, 2, 4, 256, 128, seed=23, gate_dtype=torch.float32)
+    d["x"] = torch.zeros(2, 256, dtype=torch.bfloat16)
+    d["x"][:, 3] = 2.0 ** -126
+    d["x"][:, 4] = 1.0
+    d["gate"] = torch.zeros(4, 256)
+    d["gate"][:, 3] = torch.tensor([3.4e38, -3.4e38, 3.3e38, 1.0])  # logits 4.0, -4.0, 3.9, 0
+    d["gate"][3, 4] = 5.0
+    for k in (1, 2, 3):
+        _, ids = check(d, R(k, renormalize=k > 1))
+        assert ids[0].tolist() == [3, 0, 2][:k]
+    o = on_gpu(d)
+    o["gate"][0, 4], o["gate"][1, 4] = math.inf, -math.inf
+    o["gate"][2, 4] = torch.tensor(0x7F800001, dtype=torch.int32).view(torch.float32)  # NaN in its last bit
+    # the infinite one takes the whole weight, the NaN and -inf ones are out
+    for r in (R(1), R(2, renormalize=True), R(4)):
+        out = call(o, r)
+        assert out.isfinite().all() and (out != 0).any()
+        assert torch.equal(out, call(o, R(1)))
+        assert torch.equal(out, call(dict(o, gate=o["gate"].clamp(-3.3e38, math.inf).to(torch.bfloat16)), r))
