@@ -596,7 +596,8 @@ mxq_status mxq_moe_layer_mxfp4(const void* x, int64_t M, int64_t H, int64_t I, i
  *            scales and zero points as pairs (8 N K / group bytes)
  *            16-byte aligned; concurrent calls need workspaces of their own
  *   fp32 sums; the scales multiply fp32 group sums, so the weights themselves are never rounded.
- *   The zero point is taken off as (128 + z) sum x, so an infinite x makes its row NaN.
+ *   The zero point is taken off a sum over codes with an offset, so an infinite x makes its row NaN;
+ *   finite x of any size overflow no group's sum before its value does.
  *   w_scale, w_zero, bias and out need only their element's alignment.
  *   M <= 2^19, N and K <= 2^28; M == 0 or N == 0: no-op. */
 size_t mxq_int4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group);

@@ -5,11 +5,14 @@
 // q: unsigned 4-bit codes, two per byte; one scale and (optionally) one 4-bit zero point per group
 // of G = 32, 64 or 128 elements of a row; without zero points z = 8.
 //
-// Arithmetic.  Codes become bf16 by bit pattern: 0x4300 | q is 128 + q, exactly.  So a group's
-// matrix product gives sum x (128 + q), and with X = sum x over the group
-//   sum x (q - z) = sum x (128 + q) - (128 + z) X,
-// X coming from the same matrix instruction against a column of ones.  All of it is exact up to
-// fp32 accumulation; the scale multiplies the group's fp32 sum, so no weight is ever rounded.
+// Arithmetic.  Codes become bf16 by bit pattern: 0x3b80 | q is c = 2^-8 (1 + q / 128), exactly.  So a
+// group's matrix product gives P = sum x c, and with X = sum 2^-8 x over the group
+//   2^-15 sum x (q - z) = P - (1 + z / 128) X,
+// X coming from the same matrix instruction against a column of 2^-8.  All of it is exact up to
+// fp32 accumulation; the scale multiplies the group's fp32 sum, so no weight is ever rounded, and the
+// last step multiplies by 2^15.  The 2^-8 is there for large x: a group of 128 of bf16's largest
+// value sums to less than fp32's largest, where with 0x4300 | q (128 + q) a single x of 2.4e36 overflowed
+// P and X and their difference was no number.
 //
 // Tiles: BM = 16 MT rows x BN = 64 CG columns per workgroup of four waves, each wave all rows of
 // its 16 CG columns.  Activations go through a ring of NS LDS stages (128 columns each, filled by
@@ -26,6 +29,9 @@ namespace mxq {
 
 namespace {
 
+// bf16 pairs: 2^-8 (1 + q / 128) with q in the low bits; 2^-8.
+constexpr uint32_t kI4Code = 0x3b803b80u, kI4One = 0x3b803b80u;
+constexpr float kI4Unit = 32768.f;  // sums are kept in units of 2^-15
 constexpr int kI4Threads = 256;
 constexpr int kI4Stages = 3;
 constexpr int kI4DotRows = 4;
@@ -34,14 +40,14 @@ constexpr int64_t kI4BigMaxK = 1 << 22, kI4BigMaxX = int64_t(1) << 34;
 constexpr int kI4Batch = 4, kI4MaxBatches = 16;
 constexpr int64_t kI4DotMaxK = 16384;  // eight waves of 64 blocks
 
-// Eight codes of a dword (element 0 in the lowest nibble) -> eight bf16 128 + q.
+// Eight codes of a dword (element 0 in the lowest nibble) -> eight bf16 2^-8 (1 + q / 128).
 __device__ __forceinline__ i32x4 decode8(uint32_t v) {
   const uint32_t e = v & 0x0f0f0f0fu, o = (v >> 4) & 0x0f0f0f0fu;
   i32x4 r;
-  r[0] = int(__builtin_amdgcn_perm(o, e, 0x0c040c00u) | 0x43004300u);
-  r[1] = int(__builtin_amdgcn_perm(o, e, 0x0c050c01u) | 0x43004300u);
-  r[2] = int(__builtin_amdgcn_perm(o, e, 0x0c060c02u) | 0x43004300u);
-  r[3] = int(__builtin_amdgcn_perm(o, e, 0x0c070c03u) | 0x43004300u);
+  r[0] = int(__builtin_amdgcn_perm(o, e, 0x0c040c00u) | kI4Code);
+  r[1] = int(__builtin_amdgcn_perm(o, e, 0x0c050c01u) | kI4Code);
+  r[2] = int(__builtin_amdgcn_perm(o, e, 0x0c060c02u) | kI4Code);
+  r[3] = int(__builtin_amdgcn_perm(o, e, 0x0c070c03u) | kI4Code);
   return r;
 }
 
@@ -53,6 +59,15 @@ __device__ __forceinline__ i32x4 transpose_rows(const i32x4& d) {
   const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
   const auto e = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
   return i32x4{int(c[0]), int(c[1]), int(e[0]), int(e[1])};
+}
+
+// 1 + z / 128 of a zero point, by its bits or by conversion: the same number, but the tile kernel's schedules
+// differ.  us by bits / by conversion, groups of 128: tiles of 16 rows 18.6 / 17.1 (16 x 4096 -> 16384)
+// and 26.2 / 24.3 (32 rows); of 64 rows 27.1 / 29.1 (64 x 4096 -> 16384) and 22.0 / 24.9 (128 x 2048 -> 7168).
+__device__ __forceinline__ float zero_value(uint32_t z) { return __uint_as_float(0x3f800000u | z << 16); }
+template <int MT>
+__device__ __forceinline__ float zero_value(uint32_t z) {
+  return MT == 1 ? float(128u + z) * 0.0078125f : zero_value(z);
 }
 
 // Scale i as loaded (bf16 bits or fp32 bits: nothing is done to it here, so no read has to be waited
@@ -85,8 +100,8 @@ __device__ __forceinline__ float rotate16(float v) {
 // instruction's rows would be empty, so here a lane keeps 32 columns of every x row in registers
 // and takes the same 32 columns of weight rows (one 16-byte read each, whole 1 KB pieces of a row
 // per wave) through V_DOT2_F32_BF16.  Codes pair up four apart (code i and i + 4 of a dword sit 16
-// bits apart, so one AND-OR makes two bf16 of 128 + q), x is paired the same way once.  A lane's
-// columns lie in one group: its sum, less (128 + z) times its sum of x, times the scale, is what the
+// bits apart, so one AND-OR makes two bf16), x is paired the same way once.  A lane's
+// columns lie in one group: its P, less (1 + z / 128) times its X, times the scale, is what the
 // wave adds up.  A batch is four weight rows, the next batch's reads on their way while one is
 // computed; its sums are reduced over the lanes together, halving rows and lanes at once (permlane
 // swaps), and the KW waves of a workgroup, which split K, meet in LDS at the end.
@@ -139,7 +154,7 @@ __global__ __launch_bounds__(512) void int4_dot_kernel(Int4Args a, int kw, int b
       x[m][4 * d + 2] = __builtin_amdgcn_perm(uint32_t(v[3]), uint32_t(v[1]), 0x05040100u);
       x[m][4 * d + 3] = __builtin_amdgcn_perm(uint32_t(v[3]), uint32_t(v[1]), 0x07060302u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t = dot2(x[m][4 * d + j], 0x3f803f80u, t);
+      for (int j = 0; j < 4; ++j) t = dot2(x[m][4 * d + j], kI4One, t);
     }
     xs[m] = t;
   }
@@ -154,11 +169,11 @@ __global__ __launch_bounds__(512) void int4_dot_kernel(Int4Args a, int kw, int b
       for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t c = ((uint32_t(o.w[i][d]) >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+          const uint32_t c = ((uint32_t(o.w[i][d]) >> (4 * j)) & 0x000f000fu) | kI4Code;
 #pragma unroll
           for (int m = 0; m < M; ++m) acc[m] = dot2(c, x[m][4 * d + j], acc[m]);
         }
-      const float zc = ZERO ? float(128u + ((o.z[i] >> (4 * (gi & 1))) & 15u)) : 136.f, s = scale_value<SBF>(o.s[i]);
+      const float zc = zero_value(ZERO ? (o.z[i] >> (4 * (gi & 1))) & 15u : 8u), s = scale_value<SBF>(o.s[i]);
 #pragma unroll
       for (int m = 0; m < M; ++m) v[m][i] = fmaf(-zc, xs[m], acc[m]) * s;
     }
@@ -203,9 +218,10 @@ __global__ __launch_bounds__(512) void int4_dot_kernel(Int4Args a, int kw, int b
     if (n >= a.N) continue;
     float t = 0.f;
     for (int k = 0; k < kw; ++k) t += part[k][r][m];
+    float bias = 0.f;
     if (a.bias)
-      t += a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n]) : reinterpret_cast<const float*>(a.bias)[n];
-    reinterpret_cast<uint16_t*>(a.out)[m * a.ldo + n] = f2bf(t);
+      bias = a.bias_bf16 ? bf16f(reinterpret_cast<const uint16_t*>(a.bias)[n]) : reinterpret_cast<const float*>(a.bias)[n];
+    reinterpret_cast<uint16_t*>(a.out)[m * a.ldo + n] = f2bf(fmaf(t, kI4Unit, bias));
   }
 }
 
@@ -292,7 +308,7 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
 #pragma unroll
     for (int c = 0; c < CG; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const i32x4 ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+  const i32x4 ones = {int(kI4One), int(kI4One), int(kI4One), int(kI4One)};
   auto compute = [&](int st, const Slot& v, int stage) __attribute__((always_inline)) {
     const uint8_t* as = smem + stage * STAGE + l16 * 256;
     const int blocks = min(4, (K - st * 128) / 32);
@@ -310,10 +326,10 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
         for (int i = 0; i < MPG; ++i) bf[c][i] = decode8(uint32_t(wt[c][j * MPG + i]));
         if (WIDE) {
           s[c] = SBF ? __uint_as_float(j & 1 ? v.s[c][j / 2] & 0xffff0000u : v.s[c][j / 2] << 16) : __uint_as_float(v.s[c][j]);
-          zc[c] = float(128u + ((v.z[c][0] >> (4 * j)) & 15u));
+          zc[c] = zero_value<MT>((v.z[c][0] >> (4 * j)) & 15u);
         } else {
           s[c] = scale_value<SBF>(v.s[c][j]);
-          zc[c] = float(128u + ((v.z[c][j] >> (4 * ((st * GPS + j) & 1))) & 15u));
+          zc[c] = zero_value<MT>((v.z[c][j] >> (4 * ((st * GPS + j) & 1))) & 15u);
         }
       }
 #pragma unroll
@@ -376,7 +392,7 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
       for (int r = 0; r < 4; ++r) {
         const int64_t m = m0 + mt * 16 + 4 * q + r;
         if (m >= a.M) continue;
-        const float v = acc[mt][c][r] + b;
+        const float v = fmaf(acc[mt][c][r], kI4Unit, b);
         if (a.splits > 1)
           pf[m * a.N + n] = v;
         else
@@ -389,9 +405,9 @@ __global__ __launch_bounds__(kI4Threads) void int4_tile_kernel(Int4Args a) {
 
 // A prompt is bound by the matrix instructions, so everything that is not one is taken out of the
 // loop: a pass over x first writes it with the eight columns of every 16-byte chunk in the order
-// 0 4 1 5 2 6 3 7 -- the order in which (v & 0x000f000f) | 0x43004300 and three shifts of it give
+// 0 4 1 5 2 6 3 7 -- the order in which (v & 0x000f000f) | 0x3b803b80 and three shifts of it give
 // the codes of a dword, seven instructions for eight codes -- and the groups' sums X.  The
-// product of a group starts from -(128 + z) X, so what comes out is sum x (q - z).
+// product of a group starts from -(1 + z / 128) X, so what comes out is 2^-15 sum x (q - z).
 __global__ __launch_bounds__(256) void int4_prep_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t lda,
                                                         int group, int64_t Mp, uint16_t* __restrict__ xp,
                                                         float* __restrict__ X) {
@@ -407,13 +423,13 @@ __global__ __launch_bounds__(256) void int4_prep_kernel(const uint16_t* __restri
     o.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
     o.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
     *reinterpret_cast<uint4*>(xp + m * K + c * 8) = o;
-    t = dot2(o.x, 0x3f803f80u, dot2(o.y, 0x3f803f80u, dot2(o.z, 0x3f803f80u, dot2(o.w, 0x3f803f80u, 0.f))));
+    t = dot2(o.x, kI4One, dot2(o.y, kI4One, dot2(o.z, kI4One, dot2(o.w, kI4One, 0.f))));
   }
   for (int o = 1; o < per; o <<= 1) t += __shfl_xor(t, o, kWave);
   if (m < M && (c & (per - 1)) == 0) X[(c / per) * Mp + m] = t;
 }
 
-// The scales and zero points as the large tiles take them: (s, -(128 + z)) fp32 pairs, columns
+// The scales and zero points as the large tiles take them: (s, -(1 + z / 128)) fp32 pairs, columns
 // neighbouring ([group][Np]), so that a step's arrive in LDS with one copy per group: gathered by every
 // wave from their rows, they were most of the loop's vector memory instructions.
 template <bool ZERO, bool SBF>
@@ -425,7 +441,7 @@ __global__ __launch_bounds__(256) void int4_scale_prep_kernel(Int4Args a, int64_
   for (int g = int(blockIdx.y); g < ngrp; g += int(gridDim.y)) {
     const float s = scale_value<SBF>(scale_bits<SBF>(a.s, nc * ngrp + g));
     const uint32_t z = ZERO ? (uint32_t(a.z[nc * zrow + (g >> 1)]) >> (4 * (g & 1))) & 15u : 8u;
-    sz[int64_t(g) * Np + n] = make_float2(s, -float(128u + z));
+    sz[int64_t(g) * Np + n] = make_float2(s, -zero_value(z));
   }
 }
 
@@ -513,7 +529,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
         for (int i = 0; i < FR; ++i) {
           const uint32_t u = uint32_t(w[c][h * FR + i]);
 #pragma unroll
-          for (int d = 0; d < 4; ++d) bf[c][i][d] = int(((u >> (4 * d)) & 0x000f000fu) | 0x43004300u);
+          for (int d = 0; d < 4; ++d) bf[c][i][d] = int(((u >> (4 * d)) & 0x000f000fu) | kI4Code);
         }
       }
 #pragma unroll
@@ -575,8 +591,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void int4_big_kernel(Int4Args a, co
       const int64_t m = m0 + wm * 64 + mt * 16 + 4 * q + r;
       if (m >= a.M) continue;
       uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + m * a.ldo + n;
-      const uint32_t lo = pack_bf16x2(acc[mt][0][r] + b[0], acc[mt][1][r] + b[1]);
-      const uint32_t hi = pack_bf16x2(acc[mt][2][r] + b[2], acc[mt][3][r] + b[3]);
+      const uint32_t lo = pack_bf16x2(fmaf(acc[mt][0][r], kI4Unit, b[0]), fmaf(acc[mt][1][r], kI4Unit, b[1]));
+      const uint32_t hi = pack_bf16x2(fmaf(acc[mt][2][r], kI4Unit, b[2]), fmaf(acc[mt][3][r], kI4Unit, b[3]));
       if (whole) {
         *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
       } else {

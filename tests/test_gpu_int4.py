@@ -272,3 +272,28 @@ def test_three_streams_at_once():
                 outs[i].append(ops.int4_linear(*calls[i]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(3) for o in outs[i])
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 1024), (2, 40, 256), (4, 70, 2048), (9, 70, 640), (16, 64, 2048), (64, 4100, 256),
+                                   (512, 1100, 256), (1000, 4100, 384)])
+def test_activations_of_any_size(M, N, K, G):
+    """Activations up to bf16's largest power of two, and small ones, give what the same integers give: with
+    scales scaled back every sum is that of the integer case times a power of two, so outputs are
+    equal bit for bit times 8.  One row of them all at bf16's largest value, of one sign."""
+    K = K if G == 128 else K - G
+    g = torch.Generator().manual_seed(M + N)
+    x = torch.randint(-4, 5, (M, K), generator=g)
+    w, s, z = _weights(N, K, G, N, M % 2 == 0, torch.float32, pow2=True)
+    want = _run(x.to(torch.bfloat16), w, s, z).float() * 8
+    for e in (125, 60, -100, -118):
+        out = _run((x.double() * 2.0 ** e).to(torch.bfloat16), w, (s.double() * 2.0 ** (3 - e)).float(), z)
+        assert torch.equal(out.float(), want), e
+    top = torch.finfo(torch.bfloat16).max
+    x = torch.full((M, K), 1.0, dtype=torch.bfloat16)
+    x[0] = top
+    t = (s.double() * 2.0 ** -110).float()
+    out = _run(x, w, t, z).double().numpy()
+    exact = _oracle(x, w, t, z, G)
+    mag = np.abs(x.double().numpy()) @ np.repeat(np.abs(t.double().numpy()), G, axis=1).T
+    assert (np.abs(out - exact) <= HALF * np.abs(exact) * (1 + HALF) + (G + K / G + 16) * 2.0 ** -24 * 286 * mag).all()
