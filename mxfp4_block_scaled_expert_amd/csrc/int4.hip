@@ -709,8 +709,12 @@ Int4Plan int4_plan(int64_t M, int64_t N, int64_t K, int group) {
   // 128, which cost the other kernel one more product of ones each (us, large tiles against the others:
   // 1024 x 2048 -> 7168, 224 tiles, 60 against 67 with groups of 128, 77 against 160 with 32;
   // 1024 x 4096 -> 4096, 128 tiles, 103 against 66 and 126 against 154; 700 x 7168 -> 4096, 96 tiles,
-  // groups of 64, 170 against 172; 512 x 7168 -> 2048, 32 tiles, groups of 32, 207 against 88).
-  if (K <= kI4BigMaxK && M <= kI4BigMaxX / K && cdiv(M, kBigM) * cdiv(N, kBigN) >= (group == 128 ? 192 : 128)) {
+  // groups of 64, 170 against 172; 512 x 7168 -> 2048, 32 tiles, groups of 32, 207 against 88) -- and the
+  // rows fill more than half a tile: on wide weights the grid says nothing about them (K = 4096, groups
+  // of 64: 8 rows to N = 16384 102 against 21, 64 to 28672 111 against 49, 128 to 28672 114 against
+  // 97, but 160 to 20480 109 against 172; groups of 32, 128 to 28672 144 against 135, 192 146 against
+  // 259; groups of 128, 128 to 28672 85 against 62, 160 to 24576 84 against 112).
+  if (M > kBigM / 2 && K <= kI4BigMaxK && M <= kI4BigMaxX / K && cdiv(M, kBigM) * cdiv(N, kBigN) >= (group == 128 ? 192 : 128)) {
     p.mt = 16;
     p.partial_bytes = int4_big_ws(M, N, K, group).total;
     return p;

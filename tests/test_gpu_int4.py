@@ -297,3 +297,13 @@ def test_activations_of_any_size(M, N, K, G):
     exact = _oracle(x, w, t, z, G)
     mag = np.abs(x.double().numpy()) @ np.repeat(np.abs(t.double().numpy()), G, axis=1).T
     assert (np.abs(out - exact) <= HALF * np.abs(exact) * (1 + HALF) + (G + K / G + 16) * 2.0 ** -24 * 286 * mag).all()
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(8, 16390, 256), (33, 16384, 384), (128, 24580, 128)])
+def test_few_rows_of_wide_weights(M, N, K, G):
+    g = torch.Generator().manual_seed(M + N)
+    x = torch.randint(-4, 5, (M, K), generator=g).to(torch.bfloat16)
+    w, s, z = _weights(N, K, G, N, True, torch.bfloat16, pow2=True)
+    want = torch.from_numpy(_oracle(x, w, s, z, G)).to(torch.bfloat16)
+    assert torch.equal(_run(x, w, s, z), want)

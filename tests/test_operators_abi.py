@@ -165,3 +165,16 @@ def test_binding_refuses_before_the_library():
                 dict(bias=torch.zeros(15)), dict()):
         with pytest.raises(ValueError):
             ops.int4_linear(**{**good, **bad})
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_wide_weights_do_not_bring_prompt_tiles_to_few_rows(group):
+    """The prompts' tiles of 256 rows need x laid out in the workspace (2 M K bytes and more); calls of up to
+    128 rows take partial sums at most, however wide the weights are."""
+    q = LIB.mxq_int4_linear_workspace_size
+    for M in (5, 8, 32, 64, 128):
+        for N in (16384, 28672, 131072):
+            n = q(M, N, 4096, group)
+            assert n <= 16 << 20 and n % (4 * M * N) == 0, (M, N)
+    for M in (129, 512):
+        assert q(M, 28672, 4096, group) >= 2 * M * 4096
