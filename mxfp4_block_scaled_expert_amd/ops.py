@@ -591,10 +591,25 @@ def _vector(t: Optional[torch.Tensor], n: int, name: str) -> Optional[torch.Tens
     return t.contiguous()
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """2-D rows as the kernels read them: unit last stride, 16-byte aligned, no two rows overlapping."""
-    t = _unit_last(t)
-    return t.contiguous() if t.shape[0] > 1 and t.stride(0) < t.shape[1] else t
+def _rows(t: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """bf16 2-D rows as the kernels read them, and their stride: unit last stride, 16-byte aligned, no two
+    rows overlapping.  (The stride of a single row says nothing; ``contiguous()`` keeps a misaligned
+    tensor that is contiguous.)"""
+    M, K = t.shape
+    ld, one = t.stride()
+    if M <= 1:
+        ld = K
+    if one != 1 or ld < K or ld % 8 or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format), K
+    return t, ld
+
+
+def _laid_out(t: torch.Tensor, name: str) -> torch.Tensor:
+    """A weight as the kernels read it: contiguous (copied if it is not) and 16-byte aligned."""
+    t = t.contiguous()
+    if t.data_ptr() % 16 and t.numel():
+        raise ValueError(f"{name} must start at a multiple of 16 bytes (a view at an odd offset does not)")
+    return t
 
 
 _LOGITS = {torch.float32: L.MXQ_DTYPE_F32, torch.bfloat16: L.MXQ_DTYPE_BF16}
@@ -650,17 +665,20 @@ def _moe_layer(name, weights, x, gate, router, w1, s1, w2, s2, w1_bias, gate_bia
     gb = _vector(gate_bias, E, "gate_bias")
     cb = _vector(correction_bias, E, "correction_bias")
     stream = _one_device(x, gate, w1, s1, w2, s2, b1, gb, cb, workspace, out)
-    x = _rows(x)
-    gate = gate.contiguous()
+    x, ldx = _rows(x)
+    gate, w1, w2 = _laid_out(gate, "gate"), _laid_out(w1, "w1"), _laid_out(w2, "w2")
     if out is None:
         out = x.new_empty((M, H))
+        ldo = H
     elif out.dtype != torch.bfloat16 or out.shape != (M, H) or out.stride(1) != 1 or (M > 1 and out.stride(0) < H):
         raise ValueError(f"out must be bf16 [{M}, {H}] with whole rows")
+    else:
+        ldo = out.stride(0) if M > 1 else H
     if workspace is None:
         workspace = moe_layer_workspace(M, H, I, E, router.topk, weights, x.device)
-    st = getattr(L.load(), name)(x.data_ptr(), M, H, I, E, max(x.stride(0), H), gate.data_ptr(), _LOGITS[gate.dtype],
+    st = getattr(L.load(), name)(x.data_ptr(), M, H, I, E, ldx, gate.data_ptr(), _LOGITS[gate.dtype],
                                  _ptr(gb), r, _ptr(cb), w1.data_ptr(), s1.data_ptr(), w2.data_ptr(), s2.data_ptr(),
-                                 _ptr(b1), layout, out.data_ptr(), max(out.stride(0), H), workspace.data_ptr(),
+                                 _ptr(b1), layout, out.data_ptr(), ldo, workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), stream)
     L.check(name, st)
     return out
@@ -677,8 +695,7 @@ def moe_layer_fp8(x: torch.Tensor, gate: torch.Tensor, router: Router, w1: torch
     layout = _layout(weight_layout)
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be bf16 [M, H]")
-    w1 = _as_u8(w1, "w1").contiguous()
-    w2 = _as_u8(w2, "w2").contiguous()
+    w1, w2 = _as_u8(w1, "w1"), _as_u8(w2, "w2")
     if w1_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
         raise ValueError("block scales must be fp32")
     if w1.dim() != 3:
@@ -714,8 +731,8 @@ def moe_layer_mxfp4(x: torch.Tensor, gate: torch.Tensor, router: Router, w1: tor
     else:
         rb1, rb2 = _tiled_row(H // 2), _tiled_row(I // 2)
         g1, g2 = -(-(H // 32) // 8) * 8, -(-(I // 32) // 8) * 8
-    return _moe_layer("mxq_moe_layer_mxfp4", L.MXQ_WEIGHTS_MXFP4, x, gate, router, w1.contiguous(),
-                      w1_scale.contiguous(), w2.contiguous(), w2_scale.contiguous(), w1_bias, gate_bias,
+    return _moe_layer("mxq_moe_layer_mxfp4", L.MXQ_WEIGHTS_MXFP4, x, gate, router, w1, w1_scale.contiguous(),
+                      w2, w2_scale.contiguous(), w1_bias, gate_bias,
                       correction_bias, workspace, out, layout, rb1, rb2, (E, 2 * I, g1), (E, H, g2))
 
 
@@ -751,15 +768,15 @@ def int4_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     if bias is not None and bias.numel() != N:
         raise ValueError("bias must have N elements")
     stream = _one_device(x, weight, weight_scale, weight_zero, bias)
-    x2 = _rows(x if x.dim() == 2 else x.reshape(-1, K))
+    x2, ldx = _rows(x if x.dim() == 2 else x.reshape(-1, K))
     M = x2.shape[0]
-    w, s = weight.contiguous(), weight_scale.contiguous()
+    w, s = _laid_out(weight, "weight"), weight_scale.contiguous()
     z = None if weight_zero is None else weight_zero.contiguous()
     b = None if bias is None else bias.contiguous()
     out = x2.new_empty((M, N))
     ws_bytes = _int4_bytes(M, N, K, K // groups)
     ws = x2.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
-    st = L.load().mxq_int4_linear(x2.data_ptr(), M, K, max(x2.stride(0), K), w.data_ptr(), N, K // groups, s.data_ptr(),
+    st = L.load().mxq_int4_linear(x2.data_ptr(), M, K, ldx, w.data_ptr(), N, K // groups, s.data_ptr(),
                                   _LOGITS[s.dtype], _ptr(z), _ptr(b), _bias_dtype(b), out.data_ptr(), N, _ptr(ws), ws_bytes,
                                   stream)
     L.check("mxq_int4_linear", st)

@@ -307,3 +307,15 @@ def test_few_rows_of_wide_weights(M, N, K, G):
     w, s, z = _weights(N, K, G, N, True, torch.bfloat16, pow2=True)
     want = torch.from_numpy(_oracle(x, w, s, z, G)).to(torch.bfloat16)
     assert torch.equal(_run(x, w, s, z), want)
+
+
+def test_one_row_slices_and_odd_offsets():
+    """A decoded token cut out of a wider or odd-strided buffer; contiguous rows at an odd offset."""
+    w, s, z = (t.to(gpu()) for t in _weights(40, 128, 32, 3))
+    buf = torch.randn(6 * 320 + 1, device=gpu()).to(torch.bfloat16)
+    for v in (buf[:1206].view(6, 201)[:1, :128], buf[:1920].view(6, 320)[:1, 3:131], buf[1:257].view(2, 128), buf[3:131].view(1, 128),
+              buf[3:131], buf[1:769].view(2, 3, 128), buf[1:641].view(5, 128)):
+        assert torch.equal(ops.int4_linear(v, w, s, z), ops.int4_linear(v.clone(), w, s, z))
+    odd = torch.zeros(w.numel() + 4, dtype=torch.uint8, device=gpu())[4:].view(w.shape)
+    with pytest.raises(ValueError, match="weight must start"):
+        ops.int4_linear(buf[:128], odd, s, z)

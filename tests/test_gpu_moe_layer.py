@@ -354,3 +354,23 @@ def test_fp32_router_weights_above_bf16():
         assert out.isfinite().all() and (out != 0).any()
         assert torch.equal(out, call(o, R(1)))
         assert torch.equal(out, call(dict(o, gate=o["gate"].clamp(-3.3e38, math.inf).to(torch.bfloat16)), r))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_one_row_slices_and_odd_offsets(mx):
+    """A decoded token cut out of a wider or odd-strided buffer; contiguous rows at an odd offset; a
+    misaligned weight or router is refused."""
+    d = make(mx, 4, 4, 256, 128, seed=24)
+    o = on_gpu(d)
+    r = R(2)
+    buf = torch.randn(6 * 520 + 1, device=gpu()).to(torch.bfloat16)
+    for v in (buf[:6 * 301].view(6, 301)[:1, :256], buf[:3120].view(6, 520)[:1, 3:259], buf[1:513].view(2, 256),
+              buf[5:261].view(1, 256), buf[:3 * 301].view(3, 301)[:, 8:264]):
+        assert torch.equal(call(o, r, x=v), call(o, r, x=v.clone()))
+    out = torch.full((1, 700), 3.0, dtype=torch.bfloat16, device=gpu())[:, 1:257]
+    assert torch.equal(call(o, r, x=buf[None, 5:261], out=out), call(o, r, x=buf[None, 5:261].clone()))
+    for name in ("gate", "w1", "w2"):
+        t = o[name]
+        odd = torch.zeros(t.numel() + 4, dtype=t.dtype, device=gpu())[4:].view(t.shape)
+        with pytest.raises(ValueError, match=f"{name} must start"):
+            call(dict(o, **{name: odd}), r)

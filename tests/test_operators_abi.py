@@ -178,3 +178,22 @@ def test_int4_wide_weights_do_not_bring_prompt_tiles_to_few_rows(group):
             assert n <= 16 << 20 and n % (4 * M * N) == 0, (M, N)
     for M in (129, 512):
         assert q(M, 28672, 4096, group) >= 2 * M * 4096
+
+
+def test_rows_reach_the_library_aligned():
+    """Slices of one row and contiguous views at odd offsets, which contiguous() returns as they are."""
+    bf = torch.bfloat16
+    buf = torch.arange(2 * 128 + 1).to(bf)
+    views = [torch.randn(6, 201).to(bf)[:1, :128], torch.randn(6, 320).to(bf)[:1, 3:131], torch.randn(6, 201).to(bf)[:, :128],
+             buf[1:].view(2, 128), torch.randn(1, 128).to(bf).expand(3, 128), torch.randn(128, 4).to(bf).t(),
+             torch.randn(4, 256).to(bf)[:, ::2]]
+    for v in views:
+        r, ld = ops._rows(v)
+        assert torch.equal(r, v) and r.data_ptr() % 16 == 0 and r.stride(1) == 1 and ld % 8 == 0 and ld >= 128
+        assert r.shape[0] == 1 or r.stride(0) == ld
+    for v in (torch.zeros(6, 320, dtype=bf)[:, 64:192], torch.zeros(6, 201, dtype=bf)[:1, :128], torch.zeros(4, 128, dtype=bf)):
+        assert ops._rows(v)[0].data_ptr() == v.data_ptr()  # read in place
+    odd = torch.zeros(8 * 256 + 8, dtype=torch.uint8)[8:]
+    with pytest.raises(ValueError, match="weight must start"):
+        ops._laid_out(odd.view(8, 256), "weight")
+    assert ops._laid_out(odd.view(8, 256)[:, ::2], "weight").is_contiguous()
