@@ -127,8 +127,8 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(const void* __restr
     }
   }
 
-  // ---- scores (as route_token; sigmoids with the fast exponential and reciprocal, whose errors --
-  // p (1 - p) |l| 2^-23 and 2^-23 p -- stay below the 1e-6 that the picks are allowed)
+  // ---- scores (as route_token; sigmoids with the fast exponential and reciprocal, whose errors
+  // route_err covers)
   float lmax = kNone, sum = 1.f;
   const bool need_p = by_score || (lpg && a.group_top2) || !a.renormalize;
   if (!a.sigmoid && need_p) {
@@ -200,20 +200,21 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(const void* __restr
       m1 = fmaxf(m1, o1);
     }
     const int mine = j / lpg;
-    float gs = mine < a.n_group ? (a.group_top2 && m2 > kNone ? m1 + m2 : m1) : kNone, last = kNone;
+    if (mine >= a.n_group) m1 = m2 = kNone;
+    float gs = a.group_top2 && m2 > kNone ? m1 + m2 : m1;
     bool keep = false;
-    for (int r = 0; r <= a.topk_group; ++r) {
+    for (int r = 0; r < a.topk_group; ++r) {
       const float mx = row_max(gs);
-      if (r == a.topk_group) {
-        if ((by_score || a.group_top2) && mx > kNone) close = route_near(last, mx);
-        break;
-      }
       const int g = row_min(gs == mx && mx > kNone ? mine : 64);
       if (g == mine) {
         keep = true;
         gs = kNone;
       }
-      last = mx;
+    }
+    if (by_score || a.group_top2) {
+      const RouteBounds bd = route_bounds(m1, a.group_top2 ? m2 : kNone, a.sigmoid);
+      const float out = row_max(keep ? kNone : bd.hi), in = -row_max(keep ? -bd.lo : kNone);
+      close = out > kNone && !(out < in);
     }
 #pragma unroll
     for (int i = 0; i < KPL; ++i) pick[i] = keep ? pick[i] : kNone;
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(const void* __restr
     const float mx = row_max(best);
     const bool any = mx > kNone;
     if (!__any(any)) break;
-    if (scores && k > 0 && any) close = close || route_near(last, mx);
+    if (scores && k > 0 && any) close = close || route_near(last, mx, a.sigmoid);
     last = mx;
     if (k == a.topk) break;
     int at = 1 << 20;

@@ -87,11 +87,38 @@ __device__ __forceinline__ float lane_value(float v, int src) {
 __device__ __forceinline__ float route_exp(float x) { return expf(x); }
 __device__ __forceinline__ double route_exp(double x) { return exp(x); }
 
-// The distance two fp32 picks must have to be told apart: p is within 1e-6 of itself, a sum of two
-// within its rounding.
-template <typename T>
-__device__ __forceinline__ bool route_near(T x, T y) {
-  return x - y <= T(6e-6) + T(5e-7) * (fabs(x) + fabs(y));
+// What an fp32 score p is off by at most, with u = 2^-24 a rounding.  sigmoid: the exponential (4 u of
+// itself; by the fast instruction (2 |l| + 2) u), the sum and the reciprocal leave p (1 - p) (2 |l| + 2) u +
+// 3 p u < 4 u: 2^-21 is twice that.  softmax: d = max l - l is rounded (d u of the exponential), the
+// exponential is 4 u, the sum of at most 512 of them 35 u and their own errors' mean, which is at most
+// (ln 512 + 4) u, then two more: together all scores of a token are off by less than 58 u, so 32 u for
+// either side of a comparison cover it.
+__device__ __forceinline__ float route_err(int sigmoid, int scores) {
+  return sigmoid ? float(scores) * 0x1p-21f : 0x1p-19f;
+}
+
+// Whether picks p + b may be in another order than fp32 has them, x first: each carries its score's
+// error and a rounding of itself (2^-22 leaves four).  A pick's error grows slower than the pick, so
+// looking at neighbours in the order is enough.
+__device__ __forceinline__ bool route_near(float x, float y, int sigmoid) {
+  return !(x - y > 2.f * route_err(sigmoid, 1) + 0x1p-22f * (fabsf(x) + fabsf(y)));
+}
+
+// The bounds of a group's score from its two largest terms (m2: -inf if only one counts).  Here it is
+// the terms' sizes that say what was rounded: m1 and m2 may nearly cancel, so every group has its own
+// error and no order of groups bounds it.  A sum that overflowed may be anything; an infinite
+// term (an infinite bias) is exact.
+struct RouteBounds {
+  float lo, hi;
+};
+__device__ __forceinline__ RouteBounds route_bounds(float m1, float m2, int sigmoid) {
+  const float inf = __builtin_huge_valf();
+  const bool two = m2 > -inf;
+  if (!(m1 > -inf) || m1 == inf) return {m1, m1};
+  const float v = two ? m1 + m2 : m1, mag = two ? fabsf(m1) + fabsf(m2) : fabsf(m1);
+  if (!(mag < inf)) return {-inf, inf};
+  const float e = route_err(sigmoid, two ? 2 : 1) + 0x1p-22f * mag;
+  return {v - e, v + e};
 }
 
 // A chosen expert's score relative to that of the largest chosen logit m, which is what
@@ -171,9 +198,8 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    T gs = kNone;
+    T gs = kNone, m1 = kNone, m2 = kNone;
     if (lane < a.n_group) {
-      T m1 = kNone, m2 = kNone;
       const T* v = s_val + lane * a.group_size;
 #pragma unroll 8  // reads in flight together
       for (int j = 0; j < a.group_size; ++j) {
@@ -184,18 +210,20 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
       gs = a.group_top2 && m2 > kNone ? m1 + m2 : m1;
     }
     uint64_t keep = 0;
-    T last = kNone;
-    for (int r = 0; r <= a.topk_group; ++r) {
+    for (int r = 0; r < a.topk_group; ++r) {
       const T mx = wave_max(gs);
       if (!(mx > kNone)) break;
-      if (r == a.topk_group) {
-        if (F32 && (by_score || a.group_top2)) close = close || route_near(last, mx);
-        break;
-      }
       const int g = __builtin_ctzll(__ballot(gs == mx));
       keep |= uint64_t(1) << g;
       if (lane == g) gs = kNone;
-      last = mx;
+    }
+    if (F32 && (by_score || a.group_top2)) {
+      // close: some group that was left out may score as much as one that was kept
+      const RouteBounds bd = route_bounds(float(m1), a.group_top2 ? float(m2) : -__builtin_huge_valf(), a.sigmoid);
+      const bool kept = (keep >> lane) & 1;
+      const float out = wave_max(kept ? -__builtin_huge_valf() : bd.hi);
+      const float in = -wave_max(kept ? -bd.lo : -__builtin_huge_valf());
+      close = out > -__builtin_huge_valf() && !(out < in);
     }
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
@@ -221,7 +249,9 @@ __device__ __forceinline__ RouteSlot route_token(const float (&l)[KPL], const fl
       }
     const T mx = wave_max(best);
     if (!(mx > kNone)) break;
-    if (watch && k > 0) close = close || route_near(last, mx);
+    if constexpr (F32) {
+      if (watch && k > 0) close = close || route_near(last, mx, a.sigmoid);
+    }
     last = mx;
     if (k == a.topk) break;
     const int win = __builtin_ctzll(__ballot(best == mx));

@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 RTOL = 2.0 ** -19
 
 
-def _check(logits, router, bias=None):
+def _check(logits, router, bias=None, rtol=RTOL):
     """logits: CPU tensor.  Runs the operator and compares."""
     b = None if bias is None else bias.to(gpu())
     ids, w = ops.moe_route(logits.to(gpu()), router, correction_bias=b)
@@ -30,7 +30,7 @@ def _check(logits, router, bias=None):
                                 renormalize=router.renormalize, scale=router.scale)
     assert ids.dtype == torch.int32 and w.dtype == torch.float32
     np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
-    np.testing.assert_allclose(w.double().cpu().numpy(), want_w, rtol=RTOL, atol=1e-37)
+    np.testing.assert_allclose(w.double().cpu().numpy(), want_w, rtol=rtol, atol=1e-37)
     return ids, w
 
 
@@ -205,3 +205,53 @@ def test_many_tokens_strides():
         many = ops.moe_route(wide[:, :100], r)
         assert torch.equal(few[0], many[0][:40])
         torch.testing.assert_close(few[1], many[1][:40], rtol=2 * RTOL, atol=0)
+
+
+@pytest.mark.parametrize("M", [9, 1101])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [30.0, 3e3, 1e4, 1e5, 1e7])
+def test_group_scores_whose_terms_cancel(M, scoring, big):
+    """Top-2 group scores of biases near +big and -big: what fp32 rounds off the terms is far above the
+    distance of the sums, between neighbours in the order of groups and beyond them."""
+    g = torch.Generator().manual_seed(int(big))
+    E, n = 64, 8
+    bias = torch.full((n, E // n), -2 * big)
+    bias[:, 3] = big * (1 + torch.arange(n) * 0.25)
+    bias[:, 6] = -big * (1 + torch.arange(n) * 0.25)
+    bias = bias.reshape(-1)
+    for topk_group in (1, 3, 7):
+        _check(_logits(M, E, int(big) + M), R(topk_group, scoring=scoring, n_group=n, topk_group=topk_group,
+                                             group_score="top2"), bias)
+    bias[::8] += torch.randn(n, generator=g) * big  # some groups with ordinary scores among them
+    _check(_logits(M, E, int(big) + M + 1), R(4, scoring=scoring, n_group=n, topk_group=4, group_score="top2"), bias)
+
+
+@pytest.mark.parametrize("M", [5, 1030])
+def test_group_scores_beyond_fp32(M):
+    """Sums of two terms that overflow fp32, upward and downward, are told apart; infinite biases too."""
+    big = torch.tensor([3.0e38, 3.2e38, 2.9e38, 3.3e38, -3.0e38, -3.2e38, -2.0e38, 1.0])
+    bias = (big[:, None] * torch.tensor([0.9, 1.0, 0.8, 0.99])).reshape(-1)
+    r = dict(scoring="sigmoid", n_group=8, group_score="top2")
+    for topk_group in (1, 2, 3, 5, 6, 7):
+        _check(_logits(M, 32, 60), R(4 * topk_group, topk_group=topk_group, **r), bias)
+    _check(_logits(M, 32, 61), R(4, topk_group=1, **r), -bias.abs())
+    bias = torch.zeros(32)
+    bias[[5, 21]] = math.inf
+    bias[9] = -math.inf
+    for topk_group in (1, 2, 3):
+        _check(_logits(M, 32, 62), R(2, topk_group=topk_group, **r), bias)
+
+
+@pytest.mark.parametrize("M", [40, 1500])
+@pytest.mark.parametrize("std", [4.0, 10.0])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_confident_routers(M, std, scoring):
+    """Logits so large that most scores are near 0 or 1, with no, small and ordinary biases.  A weight's
+    exponential takes the difference of two logits, which fp32 rounds by 2^-24 of it: that far apart,
+    differences of up to D add D 2^-24 to the tolerance of a weight."""
+    g = torch.Generator().manual_seed(M)
+    for bias in (torch.zeros(256), torch.randn(256, generator=g) * 1e-6, torch.randn(256, generator=g) * 0.1):
+        for r in (R(8, scoring=scoring, n_group=8, topk_group=4, group_score="top2", renormalize=True), R(8, scoring=scoring),
+                  R(6, scoring=scoring, n_group=8, topk_group=3)):
+            l = _logits(M, 256, M, std=std).clamp(max=30.0)
+            _check(l, r, bias, rtol=RTOL + float(l.max() - l.min()) * 2.0 ** -24)
