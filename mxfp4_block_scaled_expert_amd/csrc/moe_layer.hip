@@ -662,6 +662,14 @@ struct HStep {
   i32x4 v[N];
 };
 
+// What the lanes of a wave wrote to LDS before it, they read after it.  The LDS operations of a wave
+// complete in order, so there is nothing to wait for: it holds the compiler to that order.
+__device__ __forceinline__ void wave_handoff() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // LDS: tables | sums [2][slots][R][16] fp32 | h rows [8 waves][2 kDownRows][step columns] bf16
 __host__ __device__ inline int down_sum_rows(int R) {
   // segments that many waves share: fewer than eight segments of at most kDownRows rows, eight
@@ -831,7 +839,9 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_down_kernel(LayerArgs a) {
             const int r = MX ? 2 * i + (lane >> 5) : 4 * i + (lane >> 4);
             *reinterpret_cast<i32x4*>(hs + r * ROWB + (((lane & (SE / 8 - 1)) ^ r) * 16)) = hring[u].v[i];
           }
+          wave_handoff();
           wcompute_rows<WFMT, LAY>(acc, ring[u], at);
+          wave_handoff();  // before the next step's rows
         }
       }
     }
