@@ -24,6 +24,8 @@ from typing import Dict, NamedTuple, Optional, Sequence, Tuple
 
 import ctypes
 import functools
+import numbers
+import operator
 
 import torch
 
@@ -550,14 +552,29 @@ class Router(NamedTuple):
     scale: float = 1.0
 
 
+def _i32(v, name: str) -> int:
+    """v as the C struct holds it: ctypes cuts an int that does not fit, and int() a float.  (A tensor may
+    change after its struct was kept.)"""
+    try:
+        n = None if isinstance(v, torch.Tensor) else operator.index(v)
+    except TypeError:
+        n = None
+    if n is None or not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must be an int of 32 bits, got {v!r}")
+    return n
+
+
 @functools.lru_cache(maxsize=256)
 def _router_struct(r: Router):
     if r.scoring not in _SCORING:
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {r.scoring!r}")
     if r.group_score not in _GROUP_SCORE:
         raise ValueError(f"group_score must be 'max' or 'top2', got {r.group_score!r}")
-    return ctypes.byref(L.MoeRouter(int(r.topk), _SCORING[r.scoring], int(r.n_group), int(r.topk_group),
-                                    _GROUP_SCORE[r.group_score], int(bool(r.renormalize)), float(r.scale)))
+    if not isinstance(r.scale, numbers.Real):
+        raise ValueError(f"scale must be a number, got {type(r.scale).__name__}")
+    return ctypes.byref(L.MoeRouter(_i32(r.topk, "topk"), _SCORING[r.scoring], _i32(r.n_group, "n_group"),
+                                    _i32(r.topk_group, "topk_group"), _GROUP_SCORE[r.group_score],
+                                    int(bool(r.renormalize)), float(r.scale)))
 
 
 def _router(r: Router):

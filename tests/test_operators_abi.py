@@ -197,3 +197,16 @@ def test_rows_reach_the_library_aligned():
     with pytest.raises(ValueError, match="weight must start"):
         ops._laid_out(odd.view(8, 256), "weight")
     assert ops._laid_out(odd.view(8, 256)[:, ::2], "weight").is_contiguous()
+
+
+def test_router_fields_reach_the_struct_whole():
+    """Numbers that the C struct cannot hold are refused, not cut: 2^32 + 2 is not top-2, 2.5 neither."""
+    logits = torch.zeros(2, 8)
+    for bad in (dict(topk=2 ** 32 + 2), dict(topk=2.5), dict(topk=2, n_group=2 ** 32 + 1), dict(topk=2, n_group=2, topk_group=1.5),
+                dict(topk=2, topk_group=2 ** 32 + 1), dict(topk="2"), dict(topk=None)):
+        with pytest.raises(ValueError, match="32 bits"):
+            ops.moe_route(logits, ops.Router(**bad))
+    for bad in (dict(topk=torch.tensor(2)), dict(topk=2, scale=torch.tensor(2.0)), dict(topk=2, scale="1")):
+        with pytest.raises(ValueError, match="must be"):
+            ops.moe_route(logits, ops.Router(**bad))
+    assert ops._router_struct(ops.Router(3, n_group=4, topk_group=2))._obj.topk == 3
