@@ -681,6 +681,8 @@ def _moe_layer(name, weights, x, gate, router, w1, s1, w2, s2, w1_bias, gate_bia
     b1 = _vector(w1_bias, E * two_i, "w1_bias")
     gb = _vector(gate_bias, E, "gate_bias")
     cb = _vector(correction_bias, E, "correction_bias")
+    if workspace is not None and not workspace.is_contiguous():  # (elements of an expanded one share memory)
+        raise ValueError("workspace must be contiguous")
     stream = _one_device(x, gate, w1, s1, w2, s2, b1, gb, cb, workspace, out)
     x, ldx = _rows(x)
     gate, w1, w2 = _laid_out(gate, "gate"), _laid_out(w1, "w1"), _laid_out(w2, "w2")

@@ -210,3 +210,14 @@ def test_router_fields_reach_the_struct_whole():
         with pytest.raises(ValueError, match="must be"):
             ops.moe_route(logits, ops.Router(**bad))
     assert ops._router_struct(ops.Router(3, n_group=4, topk_group=2))._obj.topk == 3
+
+
+def test_workspaces_are_whole():
+    """An expanded or sliced workspace holds fewer bytes than its elements: it is refused before its size is."""
+    args = (torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(8, 256), ops.Router(2),
+            torch.zeros(8, 256, 256, dtype=torch.uint8), torch.ones(8, 2, 2), torch.zeros(8, 256, 128, dtype=torch.uint8),
+            torch.ones(8, 2, 1))
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2],
+               torch.zeros(64, 1, dtype=torch.uint8).expand(64, 1 << 16)):
+        with pytest.raises(ValueError, match="contiguous"):
+            ops.moe_layer_fp8(*args, workspace=ws)
