@@ -558,7 +558,8 @@ mxq_status mxq_moe_route(const void* logits, int32_t logits_dtype, int64_t M, in
  * Weights, scales, bias and layouts are those of mxq_fused_moe_fp8 (with bf16 activations) and
  * mxq_fused_moe_mxfp4.  The arithmetic keeps more than theirs: nothing is rounded before
  * w * silu(g) * u, which is kept as two bf16 terms (17 significant bits), so outputs agree with
- * route + fused MoE within the fused MoE's rounding.  Both layouts give bit-identical outputs.
+ * route + fused MoE within the fused MoE's rounding.  FP8 scales a block's fp32 sum of products with
+ * the codes (up to 448), as the FP8 linears do.  Both layouts give bit-identical outputs.
  *   x          bf16 [M, H], row stride ldx elements (ldx >= H, multiple of 8); 0 <= M <= 16 (0: no-op)
  *   gate       [E, H] contiguous, bf16 or fp32 (gate_dtype); gate_bias NULL or fp32 [E]
  *   out        bf16 [M, H], row stride ldo elements (ldo >= H); a token without a live expert gets zeros

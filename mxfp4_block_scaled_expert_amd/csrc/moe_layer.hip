@@ -591,7 +591,9 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
       if (i >= rows) continue;
       const float g = acc[0][r] + bg, u = acc[1][r] + bu;
       const float h = T.roww[row0 + i] * (g / (1.0f + __expf(-g)) * u);
-      const uint16_t hi = f2bf(h);
+      uint16_t hi = f2bf(h);
+      // a finite h that rounds to infinity: bf16's largest value instead, the rest is in lo
+      if ((hi & 0x7fffu) == 0x7f80u && fabsf(h) < __builtin_huge_valf()) --hi;
       const float hf = bf16f(hi);
       const uint16_t lo = f2bf(fabsf(hf) < __builtin_huge_valf() ? h - hf : 0.f);
       uint16_t* o = a.h + int64_t(row0 + i) * 2 * I + col;

@@ -374,3 +374,17 @@ def test_one_row_slices_and_odd_offsets(mx):
         odd = torch.zeros(t.numel() + 4, dtype=t.dtype, device=gpu())[4:].view(t.shape)
         with pytest.raises(ValueError, match=f"{name} must start"):
             call(dict(o, **{name: odd}), r)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_intermediate_above_bf16(sign):
+    """A finite intermediate beyond bf16's largest value stays finite in its two terms.  (MXFP4, whose
+    weights carry their scales; FP8 scales a block's fp32 sum of products with codes of up to 448,
+    which overflows from intermediates of 3.4e38 / 448 on.)"""
+    d = make(True, 2, 1, 256, 128, seed=25)
+    d["w1_bias"][:] = 0.0
+    d["w1_bias"][0, 7] = 1e20                # silu of it is itself
+    d["w1_bias"][0, 128 + 7] = sign * 3.4e18  # their product 3.4e38, between bf16's largest and fp32's
+    d["w2_scale"] = d["w2_scale"] - 20
+    out, _ = check(d, R(1))
+    assert out.isfinite().all() and out.abs().max() > 1e30
