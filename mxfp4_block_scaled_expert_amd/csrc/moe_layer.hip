@@ -367,8 +367,10 @@ __device__ __forceinline__ void wload(WStep<WFMT, G>& o, const WGeo<G>& gm, cons
   // the plain layout's 64-byte pieces want the line's other half to stay (5.1 against 5.7 TB/s)
   constexpr int kNt = TILED ? 2 : 0;
   const int q = (threadIdx.x & 63) >> 4;
-  const int wo = st * (TILED ? 2048 : 128), so = MX ? st * (TILED ? 128 : 8) : st * 4;
   const bool dead = st >= st_end;
+  // (a dead step's scalar offset could lie behind the buffer's end, of which the lanes' offsets are held
+  // to be short by just that much)
+  const int live = dead ? 0 : st, wo = live * (TILED ? 2048 : 128), so = MX ? live * (TILED ? 128 : 8) : live * 4;
   bool no0 = dead, no1 = dead, nop = dead;
   if (MX) {
     const int rest = m.K / 2 - (m.nsteps - 1) * 128 - q * 16;  // bytes of the last step from this lane's first
@@ -785,10 +787,11 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_down_kernel(LayerArgs a) {
       __attribute__((always_inline)) {
     wload<WFMT, LAY, 1>(ring[slot], w, m, st, st_end);
     const bool no = st >= st_end || (MX && st == m.nsteps - 1 && hpast);
+    const int ho = st >= st_end ? 0 : st * (SE * 2);
 #pragma unroll
     for (int i = 0; i < HStep<WFMT>::N; ++i)
       hring[slot].v[i] = __builtin_bit_cast(
-          i32x4, __builtin_amdgcn_raw_buffer_load_b128(hb, no ? kNoRead : (nx ? h1[i] : h0[i]), st * (SE * 2), 0));
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(hb, no ? kNoRead : (nx ? h1[i] : h0[i]), ho, 0));
   };
 
   // the item's rows are summed: each token's in the order of its experts, a row's shares in K order.
