@@ -19,8 +19,8 @@
 //  * moe_up_kernel: every workgroup routes all tokens itself (one wave per token: the logits are
 //    a few KB) and builds the same tables in LDS: chosen experts ascending, each with its rows
 //    (tokens ascending).  An item is 16 gate columns and the 16 matching up columns of one expert;
-//    a wave takes it over the whole K, or, where items are fewer than half the waves, two, four or
-//    eight waves share its K steps and meet in LDS.
+//    a wave takes it over the whole K; where tokens agree on few experts and items are at most a quarter
+//    of the waves, four or eight waves share an item's K steps and meet in LDS.
 //  * moe_down_kernel: a workgroup's item is 16 output columns over ALL chosen experts; its eight
 //    waves split the (segments of at most kDownRows rows of an expert) x (K steps) evenly, each
 //    fetching the h rows of its own steps through registers into a few KB of LDS of its own, and
@@ -544,14 +544,20 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
     if (tid == 0) a.rows[0] = rows;
   }
 
-  // ---- items: (chosen expert, 16 gate + 16 up columns), dealt over the workgroups first.  Where
-  // there are fewer than half as many items as waves, KS waves of a workgroup share an item, each
-  // a part of its K steps: a stream of few waves does not fill the memory system.
+  // ---- items: (chosen expert, 16 gate + 16 up columns), dealt over the workgroups first.  The grid is
+  // made for as many chosen experts as there can be; where tokens agree on a few, waves are left over,
+  // and four or eight of a workgroup share an item, each a part of its K steps, at least two (us shared / not,
+  // all tokens on the same experts: eight shares, FP8 7168 x 2048, 1 of 16 experts 74.8 / 81.8, MXFP4 7168 x
+  // 512, 1 of 8 28.0 / 35.6; four, FP8 7168 x 512, 2 of 16 35.1 / 36.1, 2048 x 1024, 2 of 8 23.4 / 23.0; two,
+  // FP8 4096 x 2048, 2 of 16 34.8 / 33.4, MXFP4 2880 x 2880, 4 of 32 31.1 / 30.0 -- MXFP4
+  // tiled, 7168 x 2048, 4 of 32 40.9 / 42.6 is the one that gained -- so two do not share).  One token's experts
+  // never leave waves over.
   const WMat m = wmat<WFMT, LAY>(a.w1, a.s1, 2 * I, H);
   const int tiles = I / 16, total = __builtin_amdgcn_readfirstlane(T.misc[1]) * tiles;
   const int waves = int(gridDim.x) * kLyWaves;
   int KS = 1;
   while (KS < kLyWaves && 2 * KS * total <= waves && 4 * KS <= m.nsteps) KS *= 2;
+  if (KS == 2) KS = 1;
   const int step = waves / KS;
   const int sub = wave & (KS - 1);
   const int st_lo = m.nsteps * sub / KS, st_hi = m.nsteps * (sub + 1) / KS;

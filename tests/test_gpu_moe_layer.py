@@ -388,3 +388,28 @@ def test_intermediate_above_bf16(sign):
     d["w2_scale"] = d["w2_scale"] - 20
     out, _ = check(d, R(1))
     assert out.isfinite().all() and out.abs().max() > 1e30
+
+
+def _shares(d, chosen, topk):
+    """Waves of a workgroup that share a gate/up item when `chosen` experts are chosen: the kernel's rule."""
+    M, H = d["x"].shape
+    E, tiles, steps = d["gate"].shape[0], d["w2"].shape[2] * (2 if d["mx"] else 1) // 16, -(-H // (256 if d["mx"] else 128))
+    waves, n = 8 * min(256, -(-min(E, M * topk) * tiles // 8)), 1
+    while n < 8 and 2 * n * chosen * tiles <= waves and 4 * n <= steps:
+        n *= 2
+    return 1 if n == 2 else n
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("M,E,H,I,topk,want", [
+    (16, 16, 2048, 128, 1, 8), (8, 8, 2176, 256, 1, 8), (16, 16, 2176, 128, 1, 8), (16, 32, 2304, 128, 2, 8),
+    (8, 8, 1024, 128, 1, 4), (4, 16, 1152, 256, 1, 4), (5, 8, 2048, 128, 2, 4), (16, 16, 640, 128, 1, 1), (2, 8, 2048, 128, 2, 1)])
+def test_tokens_that_agree_on_few_experts(mx, M, E, H, I, topk, want):
+    """Tokens on the same experts, which leave waves over that share items: eight, four or none, in steps that
+    do and do not divide by their number.  (MXFP4 at twice the columns, whose steps are twice as wide.)"""
+    H = H * 2 if mx else H
+    d = make(mx, M, E, H, I, seed=M + E + H, w1_bias=True, gate_bias=False)
+    d["x"] = d["x"][:1] * torch.exp2(torch.arange(M) % 4 - 2.0).to(torch.bfloat16)[:, None]
+    out, ids = check(d, R(topk, renormalize=True))
+    chosen = len(np.unique(ids))
+    assert chosen == topk and _shares(d, chosen, topk) == want
