@@ -49,7 +49,7 @@ struct LayerArgs {
   uint16_t* out;            // bf16 [M_all, H], row stride ldo elements
   int64_t ldo;
 };
-// Tokens one pass of the expert stages can take (their rows of x lie in LDS), and the K chunks of
+// Tokens one pass of the expert stages can take (their rows of x, and the sums of their rows, lie in LDS), and the K chunks of
 // the router product.
 int layer_pass_tokens(int wfmt, int64_t H, int32_t E, int32_t topk);
 void layer_gate_split(int32_t E, int64_t H, int32_t& S, int32_t& chunk);

@@ -923,8 +923,9 @@ void launch_layer_t(const LayerArgs& a, hipStream_t st) {
 }  // namespace
 
 int layer_pass_tokens(int wfmt, int64_t H, int32_t E, int32_t topk) {
+  const bool mx = wfmt == W_E2M1_MX;
   int m = kLayerMaxTokens;
-  while (m > 0 && up_lds(wfmt == W_E2M1_MX, H, E, topk, m) > kLyMaxLds) --m;
+  while (m > 0 && std::max(up_lds(mx, H, E, topk, m), down_lds(mx, m * topk)) > kLyMaxLds) --m;
   return m;
 }
 

@@ -413,3 +413,10 @@ def test_tokens_that_agree_on_few_experts(mx, M, E, H, I, topk, want):
     out, ids = check(d, R(topk, renormalize=True))
     chosen = len(np.unique(ids))
     assert chosen == topk and _shares(d, chosen, topk) == want
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("M,E,topk", [(16, 32, 32), (16, 64, 31), (16, 40, 29), (15, 32, 32), (1, 32, 32)])
+def test_largest_topk(mx, M, E, topk):
+    """The most rows that a call can have: the sums of the down stage's rows fill a compute unit's LDS."""
+    check(make(mx, M, E, 256, 128, seed=M + E + topk), R(topk, renormalize=True))
