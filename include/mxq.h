@@ -66,8 +66,9 @@ typedef int32_t mxq_status;
 /* Text for a status code (static storage, never NULL). */
 const char* mxq_status_string(mxq_status status);
 
-/* ABI version of this header (bumped whenever an existing signature or meaning changes; an entry
- * point that only joins the others leaves it). */
+/* ABI version of this header (bumped on any signature change or added entry point).  One exception:
+ * expert routing, the few-token MoE layer and the 4-bit linear joined version 14 without a bump, so look
+ * their symbols up (dlsym) to tell libraries with them from libraries without. */
 int32_t mxq_abi_version(void);
 
 /* Checks that `device` is a gfx950 GPU and makes it current.  Every other
