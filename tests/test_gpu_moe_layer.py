@@ -420,3 +420,33 @@ def test_tokens_that_agree_on_few_experts(mx, M, E, H, I, topk, want):
 def test_largest_topk(mx, M, E, topk):
     """The most rows that a call can have: the sums of the down stage's rows fill a compute unit's LDS."""
     check(make(mx, M, E, 256, 128, seed=M + E + topk), R(topk, renormalize=True))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_one_workspace_for_calls_in_a_row(mx):
+    """Calls one after the other on a stream may use one workspace, whatever their sizes; a call in several
+    passes, captured and replayed; out may be x itself."""
+    weights = L.MXQ_WEIGHTS_MXFP4 if mx else L.MXQ_WEIGHTS_FP8_BLOCK
+    H = 16384 if mx else 8192
+    big, small = on_gpu(make(mx, 16, 4, H, 128, seed=30)), on_gpu(make(mx, 3, 24, 256, 128, seed=31))
+    r = R(2, renormalize=True)
+    ws = ops.moe_layer_workspace(16, H, 128, 24, 2, weights, gpu())
+    want = [call(big, r), call(small, r)]
+    for _ in range(3):
+        got = [call(big, r, workspace=ws), call(small, r, workspace=ws)]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    x = big["x"].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = call(big, r, x=x, workspace=ws)
+    g = torch.Generator().manual_seed(32)
+    for rep in range(4):
+        x.copy_(torch.randn(16, H, generator=g))
+        graph.replay()
+        ref = call(big, r, x=x, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), rep
+    for o, w in ((big, want[0]), (small, want[1])):
+        y = o["x"].clone()
+        assert call(o, r, x=y, out=y).data_ptr() == y.data_ptr() and torch.equal(y, w)

@@ -255,3 +255,38 @@ def test_confident_routers(M, std, scoring):
                   R(6, scoring=scoring, n_group=8, topk_group=3)):
             l = _logits(M, 256, M, std=std).clamp(max=30.0)
             _check(l, r, bias, rtol=RTOL + float(l.max() - l.min()) * 2.0 ** -24)
+
+
+def test_captured_and_on_two_streams():
+    """Captured calls of both kernels replayed with new logits between eager calls, and both on streams of
+    their own at once."""
+    r = R(8, scoring="sigmoid", n_group=8, topk_group=4, group_score="top2", renormalize=True)
+    g = torch.Generator().manual_seed(7)
+    bias = (torch.randn(256, generator=g) * 0.1).to(gpu())
+    ls = [_logits(M, 256, 70 + M).to(gpu()) for M in (3, 2050)]
+    graphs, outs = [], []
+    for l in ls:
+        ops.moe_route(l, r, correction_bias=bias)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(ops.moe_route(l, r, correction_bias=bias))
+    for rep in range(4):
+        for l, graph, out in zip(ls, graphs, outs):
+            l.copy_(torch.randn(l.shape, generator=g) * (rep + 1))
+            graph.replay()
+            want = ops.moe_route(l, r, correction_bias=bias)
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), rep
+    want = [ops.moe_route(l, r, correction_bias=bias) for l in ls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(ops.moe_route(ls[k], r, correction_bias=bias))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for ids, w in got[k]:
+            assert torch.equal(ids, want[k][0]) and torch.equal(w, want[k][1])
