@@ -17,7 +17,8 @@
 // Tiles: BM = 16 MT rows x BN = 64 CG columns per workgroup of four waves, each wave all rows of
 // its 16 CG columns.  Activations go through a ring of NS LDS stages (128 columns each, filled by
 // direct global-to-LDS copies, 16-byte chunks XOR-swizzled by row); weights, scales and zero
-// points go straight to registers, as many steps ahead.  Where tiles are few, K is cut into chunks
+// points go straight to registers, requested as many steps ahead; once in a turn of NS steps the compiled
+// code waits for every request, so on average less is in flight.  Where tiles are few, K is cut into chunks
 // whose fp32 partial sums are added in chunk order by launch_dense_split_sum.  Up to four rows take
 // a dot-product kernel instead, prompts large tiles over x and scales laid out for them.
 #include <algorithm>
@@ -102,9 +103,11 @@ __device__ __forceinline__ float rotate16(float v) {
 // per wave) through V_DOT2_F32_BF16.  Codes pair up four apart (code i and i + 4 of a dword sit 16
 // bits apart, so one AND-OR makes two bf16), x is paired the same way once.  A lane's
 // columns lie in one group: its P, less (1 + z / 128) times its X, times the scale, is what the
-// wave adds up.  A batch is four weight rows, the next batch's reads on their way while one is
-// computed; its sums are reduced over the lanes together, halving rows and lanes at once (permlane
-// swaps), and the KW waves of a workgroup, which split K, meet in LDS at the end.
+// wave adds up.  A batch is four weight rows, in two sets of registers; the reads of a next batch hang on
+// there being one, and the compiled waits, which have to hold without it too, are for all reads, so
+// one batch is on its way at a time.  A batch's sums are reduced over the lanes together, halving rows
+// and lanes at once (permlane swaps), and the KW waves of a workgroup, which split K, meet in LDS at the
+// end.
 //
 // LPR lanes hold a row's share (64, or 32 / 16 where the share is that short: a read then covers
 // two / four rows).
@@ -450,8 +453,8 @@ __global__ __launch_bounds__(256) void int4_scale_prep_kernel(Int4Args a, int64_
 // A stage holds x, codes, group sums and pairs, all copied by DMA a step ahead: 148 to 160 KB for
 // two.  (Codes straight to registers, read by each of the four waves that use them, took 107 us
 // where this takes 92.)
-// Measured: 2048 x 2048 -> 7168 in 92 / 110 / 131 us with groups of 128 / 64 / 32, the passes over x
-// and the scales included (128: 655 TFLOP/s); the 64 x 128 and 128 x 128 tiles take 130 / 218 / 316.
+// Measured: 2048 x 2048 -> 7168 in 89 / 110 / 131 us with groups of 128 / 64 / 32, the passes over x
+// and the scales included (128: 674 TFLOP/s); the 64 x 128 and 128 x 128 tiles take 130 / 218 / 316.
 // Nothing bounds it alone: a step takes 2.4 us, its matrix instructions 0.9; without the copies it
 // is 14 % shorter, without three of four matrix instructions 10 %, without the scales' arithmetic
 // 9 %.  The two waves of a SIMD pass the same barrier and so wait together.

@@ -9,9 +9,12 @@
 // What bounds it: reading the chosen experts' weights once (a token of a 128-expert MXFP4 layer
 // with H = I = 2880 and top-4: 53 MB; of a 256-expert FP8 layer with H = 7168, I = 2048, top-8:
 // 352 MB), and for one token the latency of three dependent launches.  So both expert stages are
-// weight streams: every wave keeps a D-deep ring of 128-byte row steps in flight in registers, the
-// ring running on across its work items, and the activations come from LDS, so that no other
-// vector memory read gets between the stream's waits.
+// weight streams: every wave requests its 128-byte row steps D - 1 ahead into registers (a ring of D), on
+// across its work items, and the activations come from LDS.  In the down stage the ring stays in flight
+// as written.  In gate/up the compiled waits cut it short: MXFP4's scale codes are read in 8 or 16 bits and
+// widened at the end of each turn of D steps, where the wave waits for every request; FP8's first step
+// of a turn waits until 8 requests of 12 are left; and a w1_bias is waited for at an item's end, behind
+// the ring's requests.  Plain weights reach 3.5 to 4 TB/s there, against 5.8 in a bare read loop.
 //
 //  * moe_gate_kernel: the router product on V_MFMA_F32_16X16X32_BF16, split over experts and K;
 //    fp32 router weights are split into three bf16 terms that sum to them exactly.  Partial sums
@@ -43,9 +46,9 @@ namespace {
 constexpr int kLyThreads = 512, kLyWaves = 8;
 constexpr int kGateThreads = 256;
 constexpr int kDownRows = 4;  // rows of an expert that one pass over its weights takes in the down stage
-// Steps in the weight rings (that many less one on their way while one is multiplied).  Deeper rings
-// were measured slower for one token and no faster for many: depths 3 / 4, 4 / 6, 8 / 6 of gate-up /
-// down took 35, 36, 41 us (one MXFP4 token) and 147, 147, 152 us (16 tokens).
+// Steps in the weight rings (that many less one requested ahead).  Depths 3 / 4, 4 / 6, 8 / 6 of gate-up /
+// down took 35, 36, 41 us (one MXFP4 token) and 147, 147, 152 us (16 tokens); gate/up's turns all ended in
+// a wait for every request, so this compares no deeper ring that stays in flight.
 constexpr int kUpD = 3, kDownD = 4;
 }  // namespace
 
@@ -188,7 +191,7 @@ __device__ __forceinline__ void build_tables(const LayerArgs& a, const UpTables&
     }
     bool close;
     RouteSlot s = route_token<KPL, float>(l, b, a.rt, reinterpret_cast<float*>(scratch + wave * E), close);
-    if (__builtin_expect(close, 0)) {  // (with the hint one token's layer takes 0.2 us more than without the repeat, 0.6 us else)
+    if (__builtin_expect(close, 0)) {  // (one token's layer: 0.4 us for the repeat's code, 0.6 to 0.9 without the hint)
       bool unused;
       s = route_token<KPL, double>(l, b, a.rt, scratch + wave * E, unused);
     }
@@ -550,8 +553,8 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
   // all tokens on the same experts: eight shares, FP8 7168 x 2048, 1 of 16 experts 74.8 / 81.8, MXFP4 7168 x
   // 512, 1 of 8 28.0 / 35.6; four, FP8 7168 x 512, 2 of 16 35.1 / 36.1, 2048 x 1024, 2 of 8 23.4 / 23.0; two,
   // FP8 4096 x 2048, 2 of 16 34.8 / 33.4, MXFP4 2880 x 2880, 4 of 32 31.1 / 30.0 -- MXFP4
-  // tiled, 7168 x 2048, 4 of 32 40.9 / 42.6 is the one that gained -- so two do not share).  One token's experts
-  // never leave waves over.
+  // tiled, 7168 x 2048, 4 of 32 40.9 / 42.6 is the one that gained -- so two do not share).  One token leaves
+  // waves over only where masks leave it few experts.
   const WMat m = wmat<WFMT, LAY>(a.w1, a.s1, 2 * I, H);
   const int tiles = I / 16, total = __builtin_amdgcn_readfirstlane(T.misc[1]) * tiles;
   const int waves = int(gridDim.x) * kLyWaves;
@@ -584,7 +587,7 @@ __global__ __launch_bounds__(kLyThreads, 2) void moe_up_kernel(LayerArgs a) {
     row0 = __builtin_amdgcn_readfirstlane(T.start[ex]);
     arow = xs + uint32_t(T.row[row0 + min(l16, rows - 1)] & 0xff) * stride;
     acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // (read here, behind the ring's requests so far: in finish() the wait for it would drain the ring)
+    // (requested here and waited for in finish(), behind all of the ring's requests made meanwhile)
     if (a.b1) {
       const float* be = a.b1 + int64_t(ex) * 2 * I + nt * 16 + l16;
       bg = be[0];

@@ -1,8 +1,10 @@
 // Expert routing: router logits [M, E] -> expert ids and weights [M, topk] (route_common.hpp holds
-// the formulas).  One wave per token, four tokens per workgroup; many tokens take 16 lanes each.  Scores are computed in fp32;
-// where two picks that decide the result lie closer than fp32 scores can tell apart, the wave
-// repeats its token in 64 bits, so the chosen experts and their order are those of the exact
-// scores.
+// the formulas).  One wave per token, four tokens per workgroup; many tokens take 16 lanes each, where
+// the groups allow it.  Scores are computed in fp32; where picks that decide the result lie closer than
+// fp32 scores can tell apart, the wave repeats its token in 64 bits, so the chosen experts and their
+// order are those of the exact scores.  How many tokens that is depends on the router: 16384 x 256 in 8
+// groups, sigmoid scores, take 19 us with ordinary biases, and without any 21, 35 and 56 us as the
+// logits' deviation grows over 2, 4 and 8 (at 8 most scores are 0 or 1 to fp32).
 #include "layer.hpp"
 #include "route_common.hpp"
 
@@ -11,8 +13,8 @@ namespace mxq {
 namespace {
 constexpr int kRouteWaves = 4;
 // From here on 16 lanes per token (us, against a wave per token; 256 experts in 8 groups: 16384 tokens
-// 20.1 / 37.4, 4096 13.5 / 17.4, 1024 13.2 / 12.9, which is the length of one token's work; 128
-// experts: 16384 tokens 5.9 / 11.8, 1024 4.9 / 4.8).
+// 19.3 / 35.9, 4096 13.0 / 14.8, 2048 12.9 / 13.4, 1024 11.3 / 11.1, most of it one token repeated in
+// 64 bits; 128 experts: 16384 tokens 5.7 / 11.6, 1024 4.7 / 4.7).
 constexpr int64_t kRouteRowsFrom = 1024;
 }
 
@@ -285,6 +287,8 @@ void launch_moe_route(const void* logits, bool bf16, int64_t M, int64_t ld, cons
   if (M <= 0) return;
   const dim3 grid{unsigned(cdiv(M, kRouteWaves))}, block{256u};
   const size_t lds = a.n_group > 1 ? size_t(kRouteWaves) * a.E * 8 : 0;
+  // Lane j of 16 holds kpl experts, by E alone, so a group has to be one, two, four, ... lanes: 160
+  // experts in 8 groups of 20, for one, stay with a wave per token.
   if (M >= kRouteRowsFrom && a.topk <= 16) {
     const int kpl = a.E <= 64 ? 4 : (a.E <= 128 ? 8 : (a.E <= 256 ? 16 : 32));
     const int lpg = a.n_group > 1 ? a.group_size / kpl : 0;
