@@ -525,7 +525,8 @@ mxq_status mxq_moe_prepack_scales(const void* s, int64_t E, int64_t N, int64_t g
  *   weight   p of the chosen expert (without the bias); renormalize: divided by the sum over the
  *            token's chosen experts; times scale
  * Scores are fp32; picks closer than fp32 scores can tell apart are decided in 64 bits, so the
- * chosen experts and their order are those of the exact scores.  Weights are fp32 (2^-19 of
+ * chosen experts and their order are those of 64-bit scores.  (What 64 bits round to one value ties:
+ * sigmoids of logits from about 37 on are 1.)  Weights are fp32 (2^-19 of
  * themselves, and the logits' distance from the largest times 2^-24); a token's may differ in the last
  * bits between calls of fewer and of more than 1024 tokens, its experts do not.
  *   logits           fp32 or bf16 (logits_dtype) [M, E], row stride ldl elements (ldl >= E),

@@ -2,7 +2,7 @@
 // the formulas).  One wave per token, four tokens per workgroup; many tokens take 16 lanes each, where
 // the groups allow it.  Scores are computed in fp32; where picks that decide the result lie closer than
 // fp32 scores can tell apart, the wave repeats its token in 64 bits, so the chosen experts and their
-// order are those of the exact scores.  How many tokens that is depends on the router: 16384 x 256 in 8
+// order are those of 64-bit scores.  How many tokens that is depends on the router: 16384 x 256 in 8
 // groups, sigmoid scores, take 19 us with ordinary biases, and without any 21, 35 and 56 us as the
 // logits' deviation grows over 2, 4 and 8 (at 8 most scores are 0 or 1 to fp32).
 #include "layer.hpp"
